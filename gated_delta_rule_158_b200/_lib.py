@@ -28,6 +28,13 @@ KDA_ERR_BOUNDS = 8
 KDA_F32 = 0
 KDA_BF16 = 1
 
+KDA_ACT_NONE = 0
+KDA_ACT_SILU = 1
+KDA_NORM_RMS = 0
+KDA_NORM_L2 = 1
+KDA_ROT_HALVES = 0
+KDA_ROT_PAIRS = 1
+
 _VP = ctypes.c_void_p
 _I = ctypes.c_int
 _I64 = ctypes.c_int64
@@ -63,6 +70,28 @@ _SIGNATURES = {
     "kda_recurrent_bwd_workspace_size": (_SZ, [_I, _I, _I, _I, _I, _I]),
     "kda_recurrent_bwd": (_I, [_VP, _VP, _VP, _VP, _VP, _I, _VP, _VP, _VP, _VP, _I, _I, _I, _I,
                                _I, _I, _F, _VP, _VP, _VP, _VP, _VP, _VP, _VP, _SZ, _VP]),
+    "kda_short_conv_fwd": (_I, [_VP, _I64, _VP, _VP, _I, _VP, _VP, _I, _I, _I, _I, _I, _I, _VP,
+                                _VP, _VP, _SZ, _VP]),
+    "kda_short_conv_step": (_I, [_VP, _I64, _VP, _VP, _I, _VP, _I, _I, _I, _I, _VP, _VP]),
+    "kda_short_conv_bwd_workspace_size": (_SZ, [_I, _I, _I, _I, _I]),
+    "kda_short_conv_bwd": (_I, [_VP, _I64, _VP, _VP, _I, _VP, _VP, _VP, _VP, _I, _I, _I, _I, _I,
+                                _I, _VP, _VP, _VP, _VP, _VP, _SZ, _VP]),
+    "kda_selective_scan_fwd_workspace_size": (_SZ, [_I, _I, _I, _I, _I, _I]),
+    "kda_selective_scan_fwd": (_I, [_VP, _I64, _VP, _I64, _VP, _VP, _I64, _VP, _I64, _VP, _VP,
+                                    _I64, _VP, _I, _I, _VP, _VP, _I, _I, _I, _I, _I, _I, _VP,
+                                    _VP, _VP, _SZ, _VP]),
+    "kda_selective_scan_step": (_I, [_VP, _I64, _VP, _I64, _VP, _VP, _I64, _VP, _I64, _VP, _VP,
+                                     _I64, _VP, _I, _I, _VP, _I, _I, _I, _I, _VP, _VP]),
+    "kda_selective_scan_bwd_workspace_size": (_SZ, [_I, _I, _I, _I, _I, _I]),
+    "kda_selective_scan_bwd": (_I, [_VP, _I64, _VP, _I64, _VP, _VP, _I64, _VP, _I64, _VP, _VP,
+                                    _I64, _VP, _I, _I, _VP, _VP, _VP, _VP, _I, _I, _I, _I, _I,
+                                    _I, _VP, _VP, _VP, _VP, _VP, _VP, _VP, _VP, _VP, _VP, _SZ,
+                                    _VP]),
+    "kda_qk_norm_fwd": (_I, [_VP, _I64, _VP, _I64, _VP, _VP, _VP, _VP, _I, _I, _I, _I, _I, _I,
+                             _I, _I, _F, _VP, _VP, _VP]),
+    "kda_qk_norm_bwd_workspace_size": (_SZ, [_I, _I, _I, _I]),
+    "kda_qk_norm_bwd": (_I, [_VP, _I64, _VP, _I64, _VP, _VP, _VP, _VP, _I, _I, _I, _I, _I, _I,
+                             _I, _I, _F, _VP, _VP, _VP, _VP, _VP, _VP, _VP, _SZ, _VP]),
     "kda_get_device_status": (_I, [_VP, _VP, ctypes.POINTER(ctypes.c_int32)]),
     "kda_noalloc_get_device_status": (_I, [ctypes.POINTER(ctypes.c_int32), _VP]),
     "kda_selftest_bounded_wait": (_I, [_VP, _I64, _VP]),
@@ -332,6 +361,264 @@ def kda_recurrent_bwd(q, k, v, g, beta, dout, grads, workspace, init_state=None,
         _ptr(grads["dk"]), _ptr(grads["dv"]), _ptr(grads["dg"]), _ptr(grads["dbeta"]),
         _ptr(grads.get("d_init")), _ptr(workspace), workspace.numel() * workspace.element_size(),
         _stream(stream)), "kda_recurrent_bwd")
+
+
+# ---- the operators around the recurrence: their inputs may be row slices of
+# wider tensors, so shapes, types and devices are checked here
+
+_F32T = (torch.float32,)
+
+
+def _arg(name, t, shape, dtypes, optional=False):
+    """The tensor's pointer, after checking that it is a dense CUDA tensor of
+    this shape and type on the current device."""
+    if t is None:
+        if optional:
+            return None
+        raise TypeError(f"{name}: expected a torch.Tensor")
+    _on_device(name, t, shape, dtypes)
+    if not t.is_contiguous():
+        raise ValueError(f"{name}: expected a dense tensor")
+    return t.data_ptr()
+
+
+def _on_device(name, t, shape, dtypes):
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name}: expected a torch.Tensor")
+    if t.dtype not in dtypes:
+        raise TypeError(f"{name}: unsupported dtype {t.dtype}, expected {dtypes}")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if not t.is_cuda or t.device.index != torch.cuda.current_device():
+        raise ValueError(f"{name}: expected a tensor on the current CUDA device")
+
+
+def _like(t):
+    """The types of a tensor that has to have t's element type."""
+    _dtype(t)
+    return (t.dtype,)
+
+
+def _rows(name, t, shape, lead, dtypes):
+    """(pointer, row stride) of a tensor whose first `lead` dimensions number
+    its rows: rows dense, any constant distance apart."""
+    _on_device(name, t, shape, dtypes)
+    strides, width = t.stride(), 1
+    for n, st in zip(reversed(shape[lead:]), reversed(strides[lead:])):
+        if n > 1 and st != width:
+            raise ValueError(f"{name}: rows must be dense")
+        width *= n
+    stride = None
+    for n, st in zip(reversed(shape[:lead]), reversed(strides[:lead])):
+        if n == 1:
+            continue
+        if stride is None:
+            stride, reach = st, st * n
+        elif st != reach:
+            raise ValueError(f"{name}: rows must be a constant distance apart")
+        else:
+            reach *= n
+    if stride is None:
+        stride = width
+    if stride < width:
+        raise ValueError(f"{name}: rows overlap")
+    return t.data_ptr(), stride
+
+
+def _grad(grads, name, shape, optional=False):
+    return _arg(f"grads['{name}']", grads.get(name), shape, _F32T, optional)
+
+
+def _offsets(cu_seqlens, batch):
+    """(pointer, number of packed sequences, number of states)"""
+    if cu_seqlens is None:
+        return None, 0, batch
+    n = cu_seqlens.numel() - 1
+    return _arg("cu_seqlens", cu_seqlens, (n + 1,), (torch.int32,)), n, n
+
+
+def _scratch(workspace):
+    if workspace is None:
+        return None, 0
+    _on_device("workspace", workspace, workspace.shape, (workspace.dtype,))
+    return _ptr(workspace), workspace.numel() * workspace.element_size()
+
+
+def kda_short_conv_fwd(x, weight, out, workspace, bias=None, init_state=None, cu_seqlens=None,
+                       final_state=None, activation=KDA_ACT_SILU, stream=None):
+    """Causal convolution of each channel over its sequence's tokens; x [B,T,D]
+    (rows may be slices of a wider tensor), weight fp32 [D,W], out [B,T,D],
+    states [N,W-1,D] of x's type."""
+    B, T, D = x.shape
+    W = weight.shape[-1]
+    dt = _like(x)
+    cu, num, N = _offsets(cu_seqlens, B)
+    xp, xs = _rows("x", x, (B, T, D), 2, dt)
+    ws, wsb = _scratch(workspace)
+    _check(lib().kda_short_conv_fwd(
+        xp, xs, _arg("weight", weight, (D, W), _F32T), _arg("bias", bias, (D,), _F32T, True),
+        _dtype(x), _arg("init_state", init_state, (N, W - 1, D), dt, True), cu, num, B, T, D, W,
+        int(activation), _arg("out", out, (B, T, D), dt),
+        _arg("final_state", final_state, (N, W - 1, D), dt, True), ws, wsb, _stream(stream)),
+        "kda_short_conv_fwd")
+
+
+def kda_short_conv_step(x, weight, state, out, bias=None, activation=KDA_ACT_SILU, stream=None):
+    """One token of N sequences: x, out [N,D], state [N,W-1,D] shifted in place."""
+    N, D = x.shape
+    W = weight.shape[-1]
+    dt = _like(x)
+    xp, xs = _rows("x", x, (N, D), 1, dt)
+    _check(lib().kda_short_conv_step(
+        xp, xs, _arg("weight", weight, (D, W), _F32T), _arg("bias", bias, (D,), _F32T, True),
+        _dtype(x), _arg("state", state, (N, W - 1, D), dt), N, D, W, int(activation),
+        _arg("out", out, (N, D), dt), _stream(stream)), "kda_short_conv_step")
+
+
+def kda_short_conv_bwd_workspace_size(B, T, D, W, num_seqs=0) -> int:
+    return int(lib().kda_short_conv_bwd_workspace_size(B, T, D, W, num_seqs))
+
+
+def kda_short_conv_bwd(x, weight, dout, grads, workspace, bias=None, init_state=None,
+                       d_final=None, cu_seqlens=None, activation=KDA_ACT_SILU, stream=None):
+    """Gradients of kda_short_conv_fwd.  dout fp32 [B,T,D]; `grads` is a dict of
+    fp32 outputs dx [B,T,D], dweight [D,W] and optionally dbias [D], d_init
+    [N,W-1,D]."""
+    B, T, D = x.shape
+    W = weight.shape[-1]
+    cu, num, N = _offsets(cu_seqlens, B)
+    xp, xs = _rows("x", x, (B, T, D), 2, _like(x))
+    ws, wsb = _scratch(workspace)
+    _check(lib().kda_short_conv_bwd(
+        xp, xs, _arg("weight", weight, (D, W), _F32T), _arg("bias", bias, (D,), _F32T, True),
+        _dtype(x), _arg("init_state", init_state, (N, W - 1, D), (x.dtype,), True),
+        _arg("dout", dout, (B, T, D), _F32T),
+        _arg("d_final", d_final, (N, W - 1, D), _F32T, True), cu, num, B, T, D, W,
+        int(activation), _grad(grads, "dx", (B, T, D)), _grad(grads, "dweight", (D, W)),
+        _grad(grads, "dbias", (D,), True), _grad(grads, "d_init", (N, W - 1, D), True), ws, wsb,
+        _stream(stream)), "kda_short_conv_bwd")
+
+
+def kda_selective_scan_fwd_workspace_size(B, T, D, S, G=1, num_seqs=0) -> int:
+    return int(lib().kda_selective_scan_fwd_workspace_size(B, T, D, S, G, num_seqs))
+
+
+def _scan_inputs(x, delta, A, Bm, Cm, D, z, delta_bias, delta_softplus):
+    """The marshalled input arguments that the scan's entries share."""
+    lead, ch = tuple(x.shape[:-1]), x.shape[-1]
+    S, G = A.shape[-1], Bm.shape[-2]
+    n, dt = len(lead), _like(x)
+    args = [*_rows("x", x, (*lead, ch), n, dt), *_rows("delta", delta, (*lead, ch), n, dt),
+            _arg("A", A, (ch, S), _F32T), *_rows("Bm", Bm, (*lead, G, S), n, dt),
+            *_rows("Cm", Cm, (*lead, G, S), n, dt), _arg("D", D, (ch,), _F32T, True),
+            *((None, 0) if z is None else _rows("z", z, (*lead, ch), n, dt)),
+            _arg("delta_bias", delta_bias, (ch,), _F32T, True), int(bool(delta_softplus)),
+            _dtype(x)]
+    return args, ch, S, G
+
+
+def kda_selective_scan_fwd(x, delta, A, Bm, Cm, out, workspace, D=None, z=None, delta_bias=None,
+                           delta_softplus=True, init_state=None, cu_seqlens=None,
+                           final_state=None, stream=None):
+    """Selective state space scan; x, delta, z, out [B,T,D], Bm, Cm [B,T,G,S]
+    (inputs may be row slices of wider tensors), A fp32 [D,S], D and delta_bias
+    fp32 [D], states fp32 [N,D,S]."""
+    B, T = x.shape[:2]
+    args, ch, S, G = _scan_inputs(x, delta, A, Bm, Cm, D, z, delta_bias, delta_softplus)
+    cu, num, N = _offsets(cu_seqlens, B)
+    ws, wsb = _scratch(workspace)
+    _check(lib().kda_selective_scan_fwd(
+        *args, _arg("init_state", init_state, (N, ch, S), _F32T, True), cu, num, B, T, ch, S, G,
+        _arg("out", out, (B, T, ch), (x.dtype,)),
+        _arg("final_state", final_state, (N, ch, S), _F32T, True), ws, wsb, _stream(stream)),
+        "kda_selective_scan_fwd")
+
+
+def kda_selective_scan_step(x, delta, A, Bm, Cm, state, out, D=None, z=None, delta_bias=None,
+                            delta_softplus=True, stream=None):
+    """One token of N sequences: x, delta, z, out [N,D], Bm, Cm [N,G,S], state
+    fp32 [N,D,S] in place."""
+    N = x.shape[0]
+    args, ch, S, G = _scan_inputs(x, delta, A, Bm, Cm, D, z, delta_bias, delta_softplus)
+    _check(lib().kda_selective_scan_step(
+        *args, _arg("state", state, (N, ch, S), _F32T), N, ch, S, G,
+        _arg("out", out, (N, ch), (x.dtype,)), _stream(stream)), "kda_selective_scan_step")
+
+
+def kda_selective_scan_bwd_workspace_size(B, T, D, S, G=1, num_seqs=0) -> int:
+    return int(lib().kda_selective_scan_bwd_workspace_size(B, T, D, S, G, num_seqs))
+
+
+def kda_selective_scan_bwd(x, delta, A, Bm, Cm, dout, grads, workspace, D=None, z=None,
+                           delta_bias=None, delta_softplus=True, init_state=None, d_final=None,
+                           cu_seqlens=None, stream=None):
+    """Gradients of kda_selective_scan_fwd.  dout has x's type; `grads` is a
+    dict of fp32 outputs dx, ddelta [B,T,D], dA [D,S], dB, dC [B,T,G,S], dz
+    [B,T,D] with z, and optionally dD, ddelta_bias [D], d_init [N,D,S]."""
+    B, T = x.shape[:2]
+    args, ch, S, G = _scan_inputs(x, delta, A, Bm, Cm, D, z, delta_bias, delta_softplus)
+    cu, num, N = _offsets(cu_seqlens, B)
+    ws, wsb = _scratch(workspace)
+    _check(lib().kda_selective_scan_bwd(
+        *args, _arg("init_state", init_state, (N, ch, S), _F32T, True),
+        _arg("dout", dout, (B, T, ch), (x.dtype,)),
+        _arg("d_final", d_final, (N, ch, S), _F32T, True), cu, num, B, T, ch, S, G,
+        _grad(grads, "dx", (B, T, ch)), _grad(grads, "ddelta", (B, T, ch)),
+        _grad(grads, "dA", (ch, S)), _grad(grads, "dB", (B, T, G, S)),
+        _grad(grads, "dC", (B, T, G, S)), _grad(grads, "dD", (ch,), True),
+        _grad(grads, "dz", (B, T, ch), z is None), _grad(grads, "ddelta_bias", (ch,), True),
+        _grad(grads, "d_init", (N, ch, S), True), ws, wsb, _stream(stream)),
+        "kda_selective_scan_bwd")
+
+
+def _norm_inputs(q, k, q_weight, k_weight, positions, inv_freq, mode, rotation, eps):
+    lead, dim, dt = tuple(q.shape[:-2]), q.shape[-1], _like(q)
+    Hq, Hk, n = q.shape[-2], k.shape[-2], len(lead)
+    tokens = 1
+    for m in lead:
+        tokens *= m
+    rot = 0 if inv_freq is None else 2 * inv_freq.numel()
+    args = [*_rows("q", q, (*lead, Hq, dim), n, dt), *_rows("k", k, (*lead, Hk, dim), n, dt),
+            _arg("q_weight", q_weight, (dim,), _F32T, True),
+            _arg("k_weight", k_weight, (dim,), _F32T, True),
+            _arg("positions", positions, lead, (torch.int32,), True),
+            _arg("inv_freq", inv_freq, (rot // 2,), _F32T, True), _dtype(q), tokens, Hq, Hk, dim,
+            rot, int(mode), int(rotation), float(eps)]
+    return args, lead, Hq, Hk, dim
+
+
+def kda_qk_norm_fwd(q, k, q_out, k_out, q_weight=None, k_weight=None, positions=None,
+                    inv_freq=None, mode=KDA_NORM_L2, rotation=KDA_ROT_HALVES, eps=1e-6,
+                    stream=None):
+    """Norm of every head's query and key row, then the rotation of its first
+    2 * inv_freq.numel() elements by positions [...] (int32) times inv_freq
+    (fp32).  q [..., Hq, d], k [..., Hk, d] (rows of a token may be slices of
+    a wider tensor); q_out, k_out dense, of the same type, or q, k themselves."""
+    args, lead, Hq, Hk, dim = _norm_inputs(q, k, q_weight, k_weight, positions, inv_freq, mode,
+                                           rotation, eps)
+    _check(lib().kda_qk_norm_fwd(
+        *args, _arg("q_out", q_out, (*lead, Hq, dim), (q.dtype,)),
+        _arg("k_out", k_out, (*lead, Hk, dim), (q.dtype,)), _stream(stream)), "kda_qk_norm_fwd")
+
+
+def kda_qk_norm_bwd_workspace_size(tokens, Hq, Hk, d) -> int:
+    return int(lib().kda_qk_norm_bwd_workspace_size(tokens, Hq, Hk, d))
+
+
+def kda_qk_norm_bwd(q, k, dq_out, dk_out, grads, workspace=None, q_weight=None, k_weight=None,
+                    positions=None, inv_freq=None, mode=KDA_NORM_L2, rotation=KDA_ROT_HALVES,
+                    eps=1e-6, stream=None):
+    """Gradients of kda_qk_norm_fwd.  dq_out, dk_out fp32; `grads` is a dict of
+    fp32 outputs dq, dk (dq may be dq_out itself, dk dk_out) and optionally
+    dq_weight, dk_weight [d], which need the workspace."""
+    args, lead, Hq, Hk, dim = _norm_inputs(q, k, q_weight, k_weight, positions, inv_freq, mode,
+                                           rotation, eps)
+    ws, wsb = _scratch(workspace)
+    _check(lib().kda_qk_norm_bwd(
+        *args, _arg("dq_out", dq_out, (*lead, Hq, dim), _F32T),
+        _arg("dk_out", dk_out, (*lead, Hk, dim), _F32T), _grad(grads, "dq", (*lead, Hq, dim)),
+        _grad(grads, "dk", (*lead, Hk, dim)), _grad(grads, "dq_weight", (dim,), True),
+        _grad(grads, "dk_weight", (dim,), True), ws, wsb, _stream(stream)), "kda_qk_norm_bwd")
 
 
 def kda_get_device_status(workspace, stream=None):

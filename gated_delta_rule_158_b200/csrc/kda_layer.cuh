@@ -1,0 +1,180 @@
+// kda_layer.cuh -- what the operators around the recurrence share: argument
+// checks (spans, strides), packed-batch lookup and element-vector io.
+#pragma once
+
+#include "kda_internal.cuh"
+
+namespace kda {
+
+// ------------------------------------------------------------ host checks
+struct Span {
+  const void* p;
+  int64_t bytes;
+};
+
+inline bool spans_overlap(const Span& a, const Span& b) {
+  if (!a.p || !b.p || a.bytes <= 0 || b.bytes <= 0) return false;
+  const uintptr_t a0 = (uintptr_t)a.p, b0 = (uintptr_t)b.p;
+  return a0 < b0 + (uintptr_t)b.bytes && b0 < a0 + (uintptr_t)a.bytes;
+}
+
+inline bool span_aligned(const Span& s) { return ((uintptr_t)s.p & 15u) == 0; }
+
+// every span aligned; no output overlaps an input or another output
+template <int NI, int NO>
+kda_status check_spans(const Span (&ins)[NI], const Span (&outs)[NO]) {
+  for (const Span& s : ins)
+    if (!span_aligned(s)) return KDA_ERR_MISALIGNED;
+  for (const Span& s : outs)
+    if (!span_aligned(s)) return KDA_ERR_MISALIGNED;
+  for (int o = 0; o < NO; ++o) {
+    for (const Span& s : ins)
+      if (spans_overlap(outs[o], s)) return KDA_ERR_INVALID_ARG;
+    for (int p = 0; p < o; ++p)
+      if (spans_overlap(outs[o], outs[p])) return KDA_ERR_INVALID_ARG;
+  }
+  return KDA_OK;
+}
+
+inline int64_t elem_bytes(kda_dtype dt) { return dt == KDA_BF16 ? 2 : 4; }
+
+// bytes that `rows` rows of `width` elements, `stride` apart, span
+inline int64_t row_bytes(int64_t rows, int64_t stride, int64_t width, int64_t esz) {
+  return rows > 0 ? ((rows - 1) * stride + width) * esz : 0;
+}
+
+// a row stride covers the row, keeps 16-byte alignment and stays addressable
+inline bool stride_ok(int64_t stride, int64_t width, int64_t esz) {
+  return stride >= width && stride <= ((int64_t)1 << 31) && stride * esz % 16 == 0;
+}
+
+// B, T and the packed batch's arguments; B * T is a 32-bit row count
+inline kda_status check_batch(const int32_t* cu, int num_seqs, int B, int T) {
+  if (B <= 0 || T <= 0) return KDA_ERR_INVALID_ARG;
+  if (cu) {
+    if (B != 1 || num_seqs <= 0) return KDA_ERR_INVALID_ARG;
+  } else if (num_seqs != 0 && num_seqs != B) {
+    return KDA_ERR_INVALID_ARG;
+  }
+  if ((int64_t)B * T > 0x7fffffffLL) return KDA_ERR_UNSUPPORTED;
+  return KDA_OK;
+}
+
+// Writes the status word (OK or KDA_ERR_BAD_SEQLENS) and, where seg_off is
+// not null, seg_off[n] = number of segments of seg_len tokens in the sequences
+// before n (a sequence has at least one segment; seg_off[N] is their total).
+cudaError_t launch_seqlens_plan(const int32_t* cu, int N, int T, StatusBlock* sb, int seg_len,
+                                int32_t* seg_off, cudaStream_t stream);
+
+// ---------------------------------------------------------- device helpers
+// The last n in [0, N) with off[n] <= i, for off non-decreasing from 0 and
+// i < off[N]: of empty ranges at i it skips all, so off[n] <= i < off[n + 1].
+__device__ __forceinline__ int find_range(const int32_t* __restrict__ off, int N, int i) {
+  int lo = 0, hi = N - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (__ldg(off + mid) <= i) lo = mid;
+    else hi = mid - 1;
+  }
+  return lo;
+}
+
+// V consecutive elements as fp32 (16-byte loads where V allows); plain loads, since some
+// callers write the same rows afterwards
+template <typename T, int V>
+__device__ __forceinline__ void load_vec(const T* p, float (&v)[V]);
+
+template <>
+__device__ __forceinline__ void load_vec<float, 1>(const float* p, float (&v)[1]) {
+  v[0] = *p;
+}
+template <>
+__device__ __forceinline__ void load_vec<float, 2>(const float* p, float (&v)[2]) {
+  const float2 a = *(reinterpret_cast<const float2*>(p));
+  v[0] = a.x; v[1] = a.y;
+}
+template <>
+__device__ __forceinline__ void load_vec<float, 4>(const float* p, float (&v)[4]) {
+  const float4 a = *(reinterpret_cast<const float4*>(p));
+  v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+}
+template <>
+__device__ __forceinline__ void load_vec<float, 8>(const float* p, float (&v)[8]) {
+  const float4 a = *(reinterpret_cast<const float4*>(p));
+  const float4 b = *(reinterpret_cast<const float4*>(p) + 1);
+  v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+  v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+}
+
+__device__ __forceinline__ float2 bf2_to_f2(uint32_t u) {
+  // bf16 is the upper half of an fp32
+  return make_float2(__uint_as_float(u << 16), __uint_as_float(u & 0xffff0000u));
+}
+
+template <>
+__device__ __forceinline__ void load_vec<__nv_bfloat16, 1>(const __nv_bfloat16* p,
+                                                           float (&v)[1]) {
+  v[0] = __bfloat162float(*p);
+}
+template <>
+__device__ __forceinline__ void load_vec<__nv_bfloat16, 2>(const __nv_bfloat16* p,
+                                                           float (&v)[2]) {
+  const float2 a = bf2_to_f2(*(reinterpret_cast<const uint32_t*>(p)));
+  v[0] = a.x; v[1] = a.y;
+}
+template <>
+__device__ __forceinline__ void load_vec<__nv_bfloat16, 4>(const __nv_bfloat16* p,
+                                                           float (&v)[4]) {
+  const uint2 u = *(reinterpret_cast<const uint2*>(p));
+  const float2 a = bf2_to_f2(u.x), b = bf2_to_f2(u.y);
+  v[0] = a.x; v[1] = a.y; v[2] = b.x; v[3] = b.y;
+}
+template <>
+__device__ __forceinline__ void load_vec<__nv_bfloat16, 8>(const __nv_bfloat16* p,
+                                                           float (&v)[8]) {
+  const uint4 u = *(reinterpret_cast<const uint4*>(p));
+  const float2 a = bf2_to_f2(u.x), b = bf2_to_f2(u.y), c = bf2_to_f2(u.z), d = bf2_to_f2(u.w);
+  v[0] = a.x; v[1] = a.y; v[2] = b.x; v[3] = b.y;
+  v[4] = c.x; v[5] = c.y; v[6] = d.x; v[7] = d.y;
+}
+
+__device__ __forceinline__ uint32_t f2_to_bf2(float a, float b) {
+  const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+template <int V>
+__device__ __forceinline__ void store_vec(float* p, const float (&v)[V]) {
+  if constexpr (V == 1) {
+    *p = v[0];
+  } else if constexpr (V == 2) {
+    *reinterpret_cast<float2*>(p) = make_float2(v[0], v[1]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < V; i += 4)
+      *reinterpret_cast<float4*>(p + i) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+  }
+}
+template <int V>
+__device__ __forceinline__ void store_vec(__nv_bfloat16* p, const float (&v)[V]) {
+  if constexpr (V == 1) {
+    *p = __float2bfloat16_rn(v[0]);
+  } else if constexpr (V == 2) {
+    *reinterpret_cast<uint32_t*>(p) = f2_to_bf2(v[0], v[1]);
+  } else if constexpr (V == 4) {
+    *reinterpret_cast<uint2*>(p) = make_uint2(f2_to_bf2(v[0], v[1]), f2_to_bf2(v[2], v[3]));
+  } else {
+    static_assert(V == 8, "vector width");
+    *reinterpret_cast<uint4*>(p) = make_uint4(f2_to_bf2(v[0], v[1]), f2_to_bf2(v[2], v[3]),
+                                              f2_to_bf2(v[4], v[5]), f2_to_bf2(v[6], v[7]));
+  }
+}
+
+// 1 / (1 + e^-x): e^-x = inf gives 0, NaN stays NaN.  __expf and the fast
+// division are off by a few 2^-23 relative for |x| < 30, where the result is
+// not yet 0 or 1; a bf16 rounding is 2^-9.
+__device__ __forceinline__ float sigmoid_fast(float x) {
+  return __fdividef(1.0f, 1.0f + __expf(-x));
+}
+
+}  // namespace kda

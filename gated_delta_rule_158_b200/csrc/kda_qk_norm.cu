@@ -1,0 +1,488 @@
+// kda_qk_norm.cu -- norms of query and key rows with the position rotation,
+// forward and gradients.
+//
+//   r = 1 / sqrt(c sum x^2 + eps),  u = x r w,  out = R(position) u
+//   du = R^T dout,  dw = sum du x r,  dx = r (du w - x r c sum(du w x r))
+//
+// HBM-bound: every row is read once and written once (the gradients add one
+// fp32 row each way).  A row of d elements lies in a group of L lanes, 8
+// elements a lane, so the row's sum is log2 L shuffles and the rotation's
+// partner elements are in the same lane (pairs) or in one other lane of the
+// group (halves: rot_dim / 2 is a multiple of 8, so whole 8-element pieces
+// change places).  A block takes whole tokens, all their heads, so that the
+// angles' cosines and sines are formed once per token (fp64 product and
+// reduction to one turn, then fp32 sincospi) and read from shared memory by
+// all heads; the rows' loads are issued before they are formed.
+#include <math.h>
+
+#include "kda_layer.cuh"
+
+namespace kda {
+namespace {
+
+constexpr int kNormThreads = 256;
+constexpr int kRowsInFlight = 4;  // rows per lane group and step
+constexpr int kMaxTokens = 16;    // tokens per block (shared table: 16 x 256 floats)
+
+struct NormArgs {
+  const void* q;
+  const void* k;
+  int64_t q_stride, k_stride;
+  const float* q_weight;
+  const float* k_weight;
+  const int32_t* positions;
+  const float* inv_freq;
+  int tokens, Hq, Hk, d, rot;
+  float c, eps;
+  bool pairs;
+  void* q_out;
+  void* k_out;
+  int per_block;  // tokens per block
+  int blocks;
+  // gradients
+  const float* dq_out;
+  const float* dk_out;
+  float* dq;
+  float* dk;
+  float* partial;  // [blocks][2][d]
+};
+
+// cos and sin of positions[t0 + i] * inv_freq[j] for the block's tokens
+__device__ __forceinline__ void fill_turns(const NormArgs& a, int t0, int nt, float2* tab) {
+  const int half = a.rot >> 1;
+  for (int e = threadIdx.x; e < nt * half; e += kNormThreads) {
+    const int i = e / half, j = e - i * half;
+    // in half turns; |product| < 2^31 * inv_freq, so the fraction keeps about
+    // 2^-22 of a half turn or better for any 32-bit position at inv_freq <= 1
+    const double x = (double)a.positions[t0 + i] * (double)a.inv_freq[j] * 0.31830988618379067154;
+    const double f = x - 2.0 * rint(0.5 * x);
+    float s, co;
+    sincospif((float)f, &s, &co);
+    tab[e] = make_float2(co, s);
+  }
+}
+
+// Turns the 8 elements v of lane l (elements 8 l ..) by the table row `tab`;
+// sgn = 1 forward, -1 back.  All lanes of the warp take part.
+template <int L>
+__device__ __forceinline__ void turn(const NormArgs& a, const float2* tab, int l, float sgn,
+                                     float (&v)[8]) {
+  if (a.pairs) {
+    if (8 * l < a.rot) {
+#pragma unroll
+      for (int i = 0; i < 8; i += 2) {
+        const float2 cs = tab[4 * l + i / 2];
+        const float p = v[i], q = v[i + 1], s = sgn * cs.y;
+        v[i] = p * cs.x - q * s;
+        v[i + 1] = q * cs.x + p * s;
+      }
+    }
+    return;
+  }
+  const int hl = a.rot >> 4;  // lanes in half of the rotated part
+  const bool lo = l < hl, in = l < 2 * hl;
+  const int other = lo ? l + hl : l - hl;
+  const int src = in ? other : l;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const float o = __shfl_sync(0xffffffffu, v[i], src, L);
+    if (in) {
+      const float2 cs = tab[8 * (lo ? l : other) + i];
+      v[i] = v[i] * cs.x + (lo ? -o : o) * (sgn * cs.y);
+    }
+  }
+}
+
+template <int L>
+__device__ __forceinline__ float group_sum(float s) {
+#pragma unroll
+  for (int o = L / 2; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o, L);
+  return s;
+}
+
+template <typename Tin, int L>
+__global__ void __launch_bounds__(kNormThreads) qk_norm_fwd_kernel(const NormArgs a) {
+  extern __shared__ float2 tab[];
+  constexpr int G = kNormThreads / L;  // lane groups
+  const int l = threadIdx.x % L, grp = threadIdx.x / L;
+  const bool act = 8 * l < a.d;
+  const int t0 = blockIdx.x * a.per_block;
+  const int nt = min(a.per_block, a.tokens - t0);
+  const int H = a.Hq + a.Hk, rows = nt * H;
+  float wq[8], wk[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) wq[i] = wk[i] = 1.f;
+  if (act && a.q_weight) load_vec<float, 8>(a.q_weight + 8 * l, wq);
+  if (act && a.k_weight) load_vec<float, 8>(a.k_weight + 8 * l, wk);
+  bool filled = a.rot == 0;
+  const int steps = (rows + G * kRowsInFlight - 1) / (G * kRowsInFlight);
+  for (int s0 = 0; s0 < steps; ++s0) {
+    float x[kRowsInFlight][8];
+    int tok[kRowsInFlight], head[kRowsInFlight];
+#pragma unroll
+    for (int u = 0; u < kRowsInFlight; ++u) {
+      const int row = (s0 * kRowsInFlight + u) * G + grp;
+      tok[u] = row / H;
+      head[u] = row - tok[u] * H;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) x[u][i] = 0.f;
+      if (row < rows && act) {
+        const int64_t t = t0 + tok[u];
+        if (head[u] < a.Hq)
+          load_vec<Tin, 8>(static_cast<const Tin*>(a.q) + t * a.q_stride +
+                               (int64_t)head[u] * a.d + 8 * l, x[u]);
+        else
+          load_vec<Tin, 8>(static_cast<const Tin*>(a.k) + t * a.k_stride +
+                               (int64_t)(head[u] - a.Hq) * a.d + 8 * l, x[u]);
+      }
+    }
+    if (!filled) {
+      fill_turns(a, t0, nt, tab);
+      __syncthreads();
+      filled = true;
+    }
+#pragma unroll
+    for (int u = 0; u < kRowsInFlight; ++u) {
+      const int row = (s0 * kRowsInFlight + u) * G + grp;
+      float ss = 0.f;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) ss = fmaf(x[u][i], x[u][i], ss);
+      const float r = rsqrtf(fmaf(a.c, group_sum<L>(ss), a.eps));
+      const bool isq = head[u] < a.Hq;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) x[u][i] *= r * (isq ? wq[i] : wk[i]);
+      // rows past the end turn by the table's first token; nothing is stored
+      if (a.rot) turn<L>(a, tab + (row < rows ? tok[u] : 0) * (a.rot >> 1), l, 1.f, x[u]);
+      if (row < rows && act) {
+        const int64_t t = t0 + tok[u];
+        if (isq)
+          store_vec<8>(static_cast<Tin*>(a.q_out) + (t * a.Hq + head[u]) * a.d + 8 * l, x[u]);
+        else
+          store_vec<8>(static_cast<Tin*>(a.k_out) + (t * a.Hk + head[u] - a.Hq) * a.d + 8 * l,
+                       x[u]);
+      }
+    }
+  }
+}
+
+// Blocks walk over token tiles; a lane's share of dweight (its 8 columns, the
+// rows of its group) stays in registers over the walk, is added over the
+// block's groups in order, and leaves as one partial row per block.
+template <typename Tin, int L>
+__global__ void __launch_bounds__(kNormThreads) qk_norm_bwd_kernel(const NormArgs a) {
+  extern __shared__ float2 tab[];
+  constexpr int G = kNormThreads / L;
+  constexpr int U = 2;
+  const int l = threadIdx.x % L, grp = threadIdx.x / L;
+  const bool act = 8 * l < a.d;
+  const int H = a.Hq + a.Hk;
+  float wq[8], wk[8], gq[8], gk[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    wq[i] = wk[i] = 1.f;
+    gq[i] = gk[i] = 0.f;
+  }
+  if (act && a.q_weight) load_vec<float, 8>(a.q_weight + 8 * l, wq);
+  if (act && a.k_weight) load_vec<float, 8>(a.k_weight + 8 * l, wk);
+  for (int64_t t0 = (int64_t)blockIdx.x * a.per_block; t0 < a.tokens;
+       t0 += (int64_t)a.blocks * a.per_block) {
+    const int nt = (int)min((int64_t)a.per_block, a.tokens - t0);
+    const int rows = nt * H;
+    const int steps = (rows + G * U - 1) / (G * U);
+    if (a.rot) {
+      __syncthreads();  // the last tile's table has been read
+      fill_turns(a, (int)t0, nt, tab);
+      __syncthreads();
+    }
+    for (int s0 = 0; s0 < steps; ++s0) {
+      float x[U][8], dy[U][8];
+      int tok[U], head[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int row = (s0 * U + u) * G + grp;
+        tok[u] = row / H;
+        head[u] = row - tok[u] * H;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[u][i] = dy[u][i] = 0.f;
+        if (row < rows && act) {
+          const int64_t t = t0 + tok[u];
+          if (head[u] < a.Hq) {
+            load_vec<Tin, 8>(static_cast<const Tin*>(a.q) + t * a.q_stride +
+                                 (int64_t)head[u] * a.d + 8 * l, x[u]);
+            load_vec<float, 8>(a.dq_out + (t * a.Hq + head[u]) * a.d + 8 * l, dy[u]);
+          } else {
+            load_vec<Tin, 8>(static_cast<const Tin*>(a.k) + t * a.k_stride +
+                                 (int64_t)(head[u] - a.Hq) * a.d + 8 * l, x[u]);
+            load_vec<float, 8>(a.dk_out + (t * a.Hk + head[u] - a.Hq) * a.d + 8 * l, dy[u]);
+          }
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int row = (s0 * U + u) * G + grp;
+        float ss = 0.f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) ss = fmaf(x[u][i], x[u][i], ss);
+        const float r = rsqrtf(fmaf(a.c, group_sum<L>(ss), a.eps));
+        const bool isq = head[u] < a.Hq;
+        if (a.rot) turn<L>(a, tab + (row < rows ? tok[u] : 0) * (a.rot >> 1), l, -1.f, dy[u]);
+        float m = 0.f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          x[u][i] *= r;
+          const float g = dy[u][i] * x[u][i];
+          if (isq) gq[i] += g;  // rows past the end are zero
+          else gk[i] += g;
+          dy[u][i] *= isq ? wq[i] : wk[i];
+          m = fmaf(dy[u][i], x[u][i], m);
+        }
+        m = a.c * group_sum<L>(m);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) dy[u][i] = r * fmaf(-x[u][i], m, dy[u][i]);
+        if (row < rows && act) {
+          const int64_t t = t0 + tok[u];
+          if (isq)
+            store_vec<8>(a.dq + (t * a.Hq + head[u]) * a.d + 8 * l, dy[u]);
+          else
+            store_vec<8>(a.dk + (t * a.Hk + head[u] - a.Hq) * a.d + 8 * l, dy[u]);
+        }
+      }
+    }
+  }
+  if (!a.partial) return;
+  // [group][2][8 L] over the shared memory of the table
+  float* red = reinterpret_cast<float*>(tab);
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    red[(grp * 2 + 0) * 8 * L + 8 * l + i] = gq[i];
+    red[(grp * 2 + 1) * 8 * L + 8 * l + i] = gk[i];
+  }
+  __syncthreads();
+  for (int e = threadIdx.x; e < 2 * 8 * L; e += kNormThreads) {
+    const int which = e / (8 * L), col = e % (8 * L);
+    if (col >= a.d) continue;
+    float s = 0.f;
+    for (int g = 0; g < G; ++g) s += red[(g * 2 + which) * 8 * L + col];
+    a.partial[((int64_t)blockIdx.x * 2 + which) * a.d + col] = s;
+  }
+}
+
+// dweight column e of q or k: the blocks' partial sums, 32 lanes taking every
+// 32nd block each and a fixed tree over the lanes
+__global__ void __launch_bounds__(256) qk_norm_bwd_sum_kernel(const float* __restrict__ partial,
+                                                              int blocks, int d,
+                                                              float* __restrict__ dq_weight,
+                                                              float* __restrict__ dk_weight) {
+  const int e = blockIdx.x * 8 + threadIdx.x / 32, lane = threadIdx.x & 31;
+  if (e >= 2 * d) return;
+  float s = 0.f;
+  for (int b = lane; b < blocks; b += 32) s += partial[(int64_t)b * 2 * d + e];
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+  if (lane != 0) return;
+  if (e < d) {
+    if (dq_weight) dq_weight[e] = s;
+  } else if (dk_weight) {
+    dk_weight[e - d] = s;
+  }
+}
+
+int lane_group(int d) { return d <= 32 ? 4 : d <= 64 ? 8 : d <= 128 ? 16 : 32; }
+
+// Tokens per block: enough rows for kRowsInFlight per lane group
+int tokens_per_block(int H, int d) {
+  const int groups = kNormThreads / lane_group(d);
+  int n = groups * kRowsInFlight / H;
+  if (n > kMaxTokens) n = kMaxTokens;
+  return n < 1 ? 1 : n;
+}
+
+constexpr int kBwdBlocks = 148 * 6;
+int bwd_blocks(int tokens, int H, int d) {
+  const int per = tokens_per_block(H, d);
+  const int64_t n = ((int64_t)tokens + per - 1) / per;
+  return (int)(n < kBwdBlocks ? n : kBwdBlocks);
+}
+
+size_t table_bytes(const NormArgs& a) { return sizeof(float2) * (size_t)a.per_block * (a.rot / 2); }
+
+template <typename Tin>
+cudaError_t dispatch_fwd(const NormArgs& a, cudaStream_t st) {
+  const unsigned grid = (unsigned)(((int64_t)a.tokens + a.per_block - 1) / a.per_block);
+  const size_t sm = table_bytes(a);
+  switch (lane_group(a.d)) {
+    case 4: qk_norm_fwd_kernel<Tin, 4><<<grid, kNormThreads, sm, st>>>(a); break;
+    case 8: qk_norm_fwd_kernel<Tin, 8><<<grid, kNormThreads, sm, st>>>(a); break;
+    case 16: qk_norm_fwd_kernel<Tin, 16><<<grid, kNormThreads, sm, st>>>(a); break;
+    default: qk_norm_fwd_kernel<Tin, 32><<<grid, kNormThreads, sm, st>>>(a); break;
+  }
+  return cudaGetLastError();
+}
+
+template <typename Tin>
+cudaError_t dispatch_bwd(const NormArgs& a, cudaStream_t st) {
+  const size_t red = a.partial ? sizeof(float) * kNormThreads * 16 : 0;
+  const size_t sm = table_bytes(a) > red ? table_bytes(a) : red;
+  switch (lane_group(a.d)) {
+    case 4: qk_norm_bwd_kernel<Tin, 4><<<a.blocks, kNormThreads, sm, st>>>(a); break;
+    case 8: qk_norm_bwd_kernel<Tin, 8><<<a.blocks, kNormThreads, sm, st>>>(a); break;
+    case 16: qk_norm_bwd_kernel<Tin, 16><<<a.blocks, kNormThreads, sm, st>>>(a); break;
+    default: qk_norm_bwd_kernel<Tin, 32><<<a.blocks, kNormThreads, sm, st>>>(a); break;
+  }
+  return cudaGetLastError();
+}
+
+kda_status check_norm(const void* q, int64_t q_stride, const void* k, int64_t k_stride,
+                      const int32_t* positions, const float* inv_freq, kda_dtype dt, int tokens,
+                      int Hq, int Hk, int d, int rot_dim, kda_norm norm, kda_rotation rotation,
+                      float eps) {
+  if (!q || !k) return KDA_ERR_INVALID_ARG;
+  if (dt != KDA_F32 && dt != KDA_BF16) return KDA_ERR_INVALID_ARG;
+  if (norm != KDA_NORM_RMS && norm != KDA_NORM_L2) return KDA_ERR_INVALID_ARG;
+  if (rotation != KDA_ROT_HALVES && rotation != KDA_ROT_PAIRS) return KDA_ERR_INVALID_ARG;
+  if (tokens <= 0 || Hq <= 0 || Hk <= 0 || d <= 0 || rot_dim < 0) return KDA_ERR_INVALID_ARG;
+  if (!(eps > 0.f) || !isfinite(eps)) return KDA_ERR_INVALID_ARG;
+  if (rot_dim > d) return KDA_ERR_INVALID_ARG;
+  if ((rot_dim > 0) != (positions != nullptr) || (rot_dim > 0) != (inv_freq != nullptr))
+    return KDA_ERR_INVALID_ARG;
+  if (d % 8 != 0 || d > 256 || rot_dim % 16 != 0) return KDA_ERR_UNSUPPORTED;
+  if (Hq > (1 << 16) || Hk > (1 << 16)) return KDA_ERR_UNSUPPORTED;
+  const int64_t es = elem_bytes(dt);
+  if (!stride_ok(q_stride, (int64_t)Hq * d, es) || !stride_ok(k_stride, (int64_t)Hk * d, es))
+    return KDA_ERR_INVALID_ARG;
+  return KDA_OK;
+}
+
+NormArgs norm_args(const void* q, int64_t q_stride, const void* k, int64_t k_stride,
+                   const float* q_weight, const float* k_weight, const int32_t* positions,
+                   const float* inv_freq, int tokens, int Hq, int Hk, int d, int rot_dim,
+                   kda_norm norm, kda_rotation rotation, float eps) {
+  NormArgs a{};
+  a.q = q;
+  a.k = k;
+  a.q_stride = q_stride;
+  a.k_stride = k_stride;
+  a.q_weight = q_weight;
+  a.k_weight = k_weight;
+  a.positions = positions;
+  a.inv_freq = inv_freq;
+  a.tokens = tokens;
+  a.Hq = Hq;
+  a.Hk = Hk;
+  a.d = d;
+  a.rot = rot_dim;
+  a.c = norm == KDA_NORM_RMS ? 1.0f / (float)d : 1.0f;
+  a.eps = eps;
+  a.pairs = rotation == KDA_ROT_PAIRS;
+  a.per_block = tokens_per_block(Hq + Hk, d);
+  return a;
+}
+
+}  // namespace
+}  // namespace kda
+
+using namespace kda;
+
+extern "C" {
+
+kda_status kda_qk_norm_fwd(const void* q, int64_t q_stride, const void* k, int64_t k_stride,
+                           const float* q_weight, const float* k_weight,
+                           const int32_t* positions, const float* inv_freq, kda_dtype in_dtype,
+                           int tokens, int Hq, int Hk, int d, int rot_dim, kda_norm norm,
+                           kda_rotation rotation, float eps, void* q_out, void* k_out,
+                           void* stream) {
+  if (!q_out || !k_out) return KDA_ERR_INVALID_ARG;
+  if (kda_status s = check_norm(q, q_stride, k, k_stride, positions, inv_freq, in_dtype, tokens,
+                                Hq, Hk, d, rot_dim, norm, rotation, eps))
+    return s;
+  const int64_t es = elem_bytes(in_dtype), n = tokens;
+  const int64_t wq = (int64_t)Hq * d, wk = (int64_t)Hk * d;
+  // in place: a dense input that is its own output is read before it is written
+  const bool q_in_place = q == q_out && q_stride == wq;
+  const bool k_in_place = k == k_out && k_stride == wk;
+  const Span qs = {q, row_bytes(n, q_stride, wq, es)}, ks = {k, row_bytes(n, k_stride, wk, es)};
+  const Span qo = {q_out, n * wq * es}, ko = {k_out, n * wk * es};
+  const Span ins[] = {{q_weight, (int64_t)d * 4},
+                      {k_weight, (int64_t)d * 4},
+                      {positions, n * 4},
+                      {inv_freq, (int64_t)rot_dim * 2}};
+  const Span outs[] = {qo, ko};
+  if (kda_status s = check_spans(ins, outs)) return s;
+  if (!span_aligned(qs) || !span_aligned(ks)) return KDA_ERR_MISALIGNED;
+  if ((!q_in_place && spans_overlap(qo, qs)) || (!k_in_place && spans_overlap(ko, ks)) ||
+      spans_overlap(qo, ks) || spans_overlap(ko, qs))
+    return KDA_ERR_INVALID_ARG;
+  NormArgs a = norm_args(q, q_stride, k, k_stride, q_weight, k_weight, positions, inv_freq,
+                         tokens, Hq, Hk, d, rot_dim, norm, rotation, eps);
+  a.q_out = q_out;
+  a.k_out = k_out;
+  cudaStream_t st = (cudaStream_t)stream;
+  const cudaError_t e = in_dtype == KDA_BF16 ? dispatch_fwd<__nv_bfloat16>(a, st)
+                                             : dispatch_fwd<float>(a, st);
+  return e == cudaSuccess ? KDA_OK : cuda_failure(e);
+}
+
+size_t kda_qk_norm_bwd_workspace_size(int tokens, int Hq, int Hk, int d) {
+  if (tokens <= 0 || Hq <= 0 || Hk <= 0 || d <= 0 || d % 8 != 0 || d > 256 || Hq > (1 << 16) ||
+      Hk > (1 << 16))
+    return 0;
+  return sizeof(float) * (size_t)bwd_blocks(tokens, Hq + Hk, d) * 2 * d;
+}
+
+kda_status kda_qk_norm_bwd(const void* q, int64_t q_stride, const void* k, int64_t k_stride,
+                           const float* q_weight, const float* k_weight,
+                           const int32_t* positions, const float* inv_freq, kda_dtype in_dtype,
+                           int tokens, int Hq, int Hk, int d, int rot_dim, kda_norm norm,
+                           kda_rotation rotation, float eps, const float* dq_out,
+                           const float* dk_out, float* dq, float* dk, float* dq_weight,
+                           float* dk_weight, void* workspace, size_t workspace_bytes,
+                           void* stream) {
+  if (!dq_out || !dk_out || !dq || !dk) return KDA_ERR_INVALID_ARG;
+  if ((dq_weight && !q_weight) || (dk_weight && !k_weight)) return KDA_ERR_INVALID_ARG;
+  if (kda_status s = check_norm(q, q_stride, k, k_stride, positions, inv_freq, in_dtype, tokens,
+                                Hq, Hk, d, rot_dim, norm, rotation, eps))
+    return s;
+  const bool sums = dq_weight || dk_weight;
+  const size_t need = sums ? kda_qk_norm_bwd_workspace_size(tokens, Hq, Hk, d) : 0;
+  if (sums && !workspace) return KDA_ERR_WORKSPACE;
+  const int64_t es = elem_bytes(in_dtype), n = tokens;
+  const int64_t wq = (int64_t)Hq * d, wk = (int64_t)Hk * d;
+  const Span dqo = {dq_out, n * wq * 4}, dko = {dk_out, n * wk * 4};
+  const Span dqs = {dq, n * wq * 4}, dks = {dk, n * wk * 4};
+  const Span ins[] = {{q, row_bytes(n, q_stride, wq, es)},
+                      {k, row_bytes(n, k_stride, wk, es)},
+                      {q_weight, (int64_t)d * 4},
+                      {k_weight, (int64_t)d * 4},
+                      {positions, n * 4},
+                      {inv_freq, (int64_t)rot_dim * 2}};
+  const Span outs[] = {dqs, dks, {dq_weight, (int64_t)d * 4}, {dk_weight, (int64_t)d * 4},
+                       {sums ? workspace : nullptr, (int64_t)need}};
+  if (kda_status s = check_spans(ins, outs)) return s;
+  if (!span_aligned(dqo) || !span_aligned(dko)) return KDA_ERR_MISALIGNED;
+  for (int i = 0; i < 5; ++i) {
+    // dq may overwrite dq_out and dk dk_out, exactly
+    if (!(i == 0 && dq == dq_out) && spans_overlap(outs[i], dqo)) return KDA_ERR_INVALID_ARG;
+    if (!(i == 1 && dk == dk_out) && spans_overlap(outs[i], dko)) return KDA_ERR_INVALID_ARG;
+  }
+  if (workspace_bytes < need) return KDA_ERR_WORKSPACE;
+  NormArgs a = norm_args(q, q_stride, k, k_stride, q_weight, k_weight, positions, inv_freq,
+                         tokens, Hq, Hk, d, rot_dim, norm, rotation, eps);
+  a.dq_out = dq_out;
+  a.dk_out = dk_out;
+  a.dq = dq;
+  a.dk = dk;
+  a.partial = sums ? static_cast<float*>(workspace) : nullptr;
+  a.blocks = bwd_blocks(tokens, Hq + Hk, d);
+  cudaStream_t st = (cudaStream_t)stream;
+  cudaError_t e = in_dtype == KDA_BF16 ? dispatch_bwd<__nv_bfloat16>(a, st)
+                                       : dispatch_bwd<float>(a, st);
+  if (e == cudaSuccess && sums) {
+    qk_norm_bwd_sum_kernel<<<(unsigned)((2 * d + 7) / 8), 256, 0, st>>>(
+        a.partial, a.blocks, d, dq_weight, dk_weight);
+    e = cudaGetLastError();
+  }
+  return e == cudaSuccess ? KDA_OK : cuda_failure(e);
+}
+
+}  // extern "C"

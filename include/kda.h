@@ -375,6 +375,214 @@ KDA_API kda_status kda_recurrent_bwd(const void *q, const void *k, const void *v
                              float *dv_out, float *dg, float *dbeta, float *d_init,
                              void *workspace, size_t workspace_bytes, void *stream);
 
+/* ------------------------------------------------------------------------
+ * The operators around the recurrence: the short causal convolution and the
+ * per-head norms that make its q, k and v, and the selective state space
+ * scan, a recurrence with a diagonal state.  The conventions above hold, with
+ * these additions:
+ *  - A *_stride argument is the distance in elements between the rows of two
+ *    consecutive tokens of that input (rows of a wider tensor may be passed
+ *    in place; the row itself is dense), the same across the batch: token t
+ *    of sequence b is row b * T + t.  It is at least the row's length and a
+ *    multiple of 16 bytes.  Outputs are dense.
+ *  - Cotangents and gradients are fp32 where the entry says so; every sum of
+ *    a gradient runs in a fixed order, so results are deterministic.
+ *  - No output may overlap an input or another output, unless the entry says
+ *    so (KDA_ERR_INVALID_ARG).
+ *  - cu_seqlens, num_seqs: as kda_chunk_fwd.  Malformed offsets are reported
+ *    on the device (KDA_ERR_BAD_SEQLENS) and no output is written.
+ * ------------------------------------------------------------------------ */
+
+typedef enum kda_activation { KDA_ACT_NONE = 0, KDA_ACT_SILU = 1 } kda_activation;
+
+/*
+ * Short causal convolution of each channel over the tokens of its sequence:
+ *   p[t, d] = bias[d] + sum_{j < W} weight[d, j] x[t - (W - 1) + j, d],
+ *   out     = p, or p Sigmoid(p) with KDA_ACT_SILU,
+ * where the W - 1 rows before a sequence's first token are the rows of its
+ * init_state (oldest first), or zeros.
+ *  x           : in_dtype [B, T, D] rows, x_stride apart
+ *  weight      : fp32 [D, W];  bias : fp32 [D] or NULL
+ *  init_state  : in_dtype [N, W - 1, D] or NULL (N = num_seqs or B)
+ *  out         : in_dtype [B, T, D]
+ *  final_state : in_dtype [N, W - 1, D] or NULL: the last W - 1 rows of
+ *                (init_state rows, then x rows) of each sequence, so that a
+ *                later call or kda_short_conv_step continues from it
+ *  workspace   : >= 256 bytes (the device status word, cleared by this call)
+ * Arithmetic is fp32; out is rounded once.
+ * Supported: W in {2, 3, 4}, D a multiple of 8, B * T < 2^31.
+ */
+KDA_API kda_status kda_short_conv_fwd(const void *x, int64_t x_stride, const float *weight,
+                              const float *bias, kda_dtype in_dtype, const void *init_state,
+                              const int32_t *cu_seqlens, int num_seqs, int B, int T, int D,
+                              int W, kda_activation activation, void *out, void *final_state,
+                              void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * One token of kda_short_conv_fwd for N sequences: out from the state's rows
+ * and x, then the state shifted by one row in place (its oldest row leaves, x
+ * enters).
+ *  x : in_dtype [N, D] rows, x_stride apart;  out : in_dtype [N, D]
+ *  state : in_dtype [N, W - 1, D], read and written
+ */
+KDA_API kda_status kda_short_conv_step(const void *x, int64_t x_stride, const float *weight,
+                               const float *bias, kda_dtype in_dtype, void *state, int N,
+                               int D, int W, kda_activation activation, void *out,
+                               void *stream);
+
+/*
+ * Gradients of kda_short_conv_fwd.  With ds = dout act'(p):
+ *   dx[s] = sum_j weight[:, j] ds[s + W - 1 - j] (+ d_final where the row is
+ *           kept), d_init likewise for the rows of init_state,
+ *   dweight[:, j] = sum_t ds[t] x[t - (W - 1) + j],  dbias = sum_t ds[t].
+ *  dout    : fp32 [B, T, D];  d_final : fp32 [N, W - 1, D] or NULL (zeros)
+ *  dx      : fp32 [B, T, D];  dweight : fp32 [D, W]
+ *  dbias   : fp32 [D] or NULL;  d_init : fp32 [N, W - 1, D] or NULL
+ *  workspace : kda_short_conv_bwd_workspace_size bytes (status word, partial
+ *            sums of dweight and dbias; 0 for unsupported sizes)
+ */
+KDA_API size_t kda_short_conv_bwd_workspace_size(int B, int T, int D, int W, int num_seqs);
+
+KDA_API kda_status kda_short_conv_bwd(const void *x, int64_t x_stride, const float *weight,
+                              const float *bias, kda_dtype in_dtype, const void *init_state,
+                              const float *dout, const float *d_final,
+                              const int32_t *cu_seqlens, int num_seqs, int B, int T, int D,
+                              int W, kda_activation activation, float *dx, float *dweight,
+                              float *dbias, float *d_init, void *workspace,
+                              size_t workspace_bytes, void *stream);
+
+/*
+ * Selective state space scan: every channel d holds a state of S values that
+ * decays and takes its input by gates computed from the token,
+ *   dt  = delta[t, d] + delta_bias[d], through log(1 + e^dt) with delta_softplus,
+ *   h_t[d, s] = exp(dt A[d, s]) h_{t-1}[d, s] + dt x[t, d] Bm[t, g, s],
+ *   y[t, d]   = sum_s Cm[t, g, s] h_t[d, s] + D_skip[d] x[t, d],
+ *   out       = y, or y z Sigmoid(z) with z given,      g = d / (D / G).
+ *  x, delta, z : in_dtype [B, T, D] rows (z may be NULL)
+ *  Bm, Cm      : in_dtype [B, T, G, S] rows of G * S
+ *  A           : fp32 [D, S] (negative where the state decays)
+ *  D_skip, delta_bias : fp32 [D] or NULL (zeros)
+ *  init_state, final_state : fp32 [N, D, S] or NULL (N = num_seqs or B); they
+ *                may be the same buffer, as in kda_chunk_fwd
+ *  out         : in_dtype [B, T, D]
+ *  workspace   : kda_selective_scan_fwd_workspace_size bytes (status word,
+ *                and the states between the segments of a long sequence,
+ *                which run side by side; 0 for unsupported sizes)
+ * States and sums are fp32; out is rounded once.  A zero-length sequence has
+ * final = init.
+ * Supported: S in {8, 16, 32, 64, 128}; D a multiple of 8; G dividing D, with
+ * D / G a multiple of 32 where G > 1; B * T < 2^31.
+ */
+KDA_API size_t kda_selective_scan_fwd_workspace_size(int B, int T, int D, int S, int G,
+                                                     int num_seqs);
+
+KDA_API kda_status kda_selective_scan_fwd(const void *x, int64_t x_stride, const void *delta,
+                                  int64_t delta_stride, const float *A, const void *Bm,
+                                  int64_t B_stride, const void *Cm, int64_t C_stride,
+                                  const float *D_skip, const void *z, int64_t z_stride,
+                                  const float *delta_bias, int delta_softplus,
+                                  kda_dtype in_dtype, const float *init_state,
+                                  const int32_t *cu_seqlens, int num_seqs, int B, int T,
+                                  int D, int S, int G, void *out, float *final_state,
+                                  void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * One token of the scan for N sequences, the state updated in place (as
+ * kda_decode_step).  x, delta, z, out : [N, D];  Bm, Cm : [N, G, S];
+ * state : fp32 [N, D, S], read and written once.  No workspace is needed.
+ */
+KDA_API kda_status kda_selective_scan_step(const void *x, int64_t x_stride, const void *delta,
+                                   int64_t delta_stride, const float *A, const void *Bm,
+                                   int64_t B_stride, const void *Cm, int64_t C_stride,
+                                   const float *D_skip, const void *z, int64_t z_stride,
+                                   const float *delta_bias, int delta_softplus,
+                                   kda_dtype in_dtype, float *state, int N, int D, int S,
+                                   int G, void *out, void *stream);
+
+/*
+ * Gradients of kda_selective_scan_fwd.  With g_t = dL/dh_t (dout carried back
+ * through the gate, the skip and the decays, plus d_final at a sequence's
+ * end):
+ *   dCm = sum_d h dy, dBm = sum_d g dt x, dx = dt sum_s g Bm + D_skip dy,
+ *   d(dt) = sum_s (g exp(dt A) h_{t-1} A) + x sum_s g Bm,
+ *   dA = sum_t g exp(dt A) h_{t-1} dt,  dz = dout y (z Sigmoid(z))', ...
+ * The states are computed again from the inputs.
+ *  dout  : in_dtype [B, T, D];  d_final : fp32 [N, D, S] or NULL (zeros)
+ * Outputs, fp32, written whole (NULL where marked to skip):
+ *  dx, ddelta : [B, T, D];  dA : [D, S];  dBm, dCm : [B, T, G, S]
+ *  dD_skip, ddelta_bias : [D] or NULL;  dz : [B, T, D], given with z;
+ *  d_init : [N, D, S] or NULL
+ *  workspace : kda_selective_scan_bwd_workspace_size bytes
+ */
+KDA_API size_t kda_selective_scan_bwd_workspace_size(int B, int T, int D, int S, int G,
+                                                     int num_seqs);
+
+KDA_API kda_status kda_selective_scan_bwd(const void *x, int64_t x_stride, const void *delta,
+                                  int64_t delta_stride, const float *A, const void *Bm,
+                                  int64_t B_stride, const void *Cm, int64_t C_stride,
+                                  const float *D_skip, const void *z, int64_t z_stride,
+                                  const float *delta_bias, int delta_softplus,
+                                  kda_dtype in_dtype, const float *init_state,
+                                  const void *dout, const float *d_final,
+                                  const int32_t *cu_seqlens, int num_seqs, int B, int T,
+                                  int D, int S, int G, float *dx, float *ddelta, float *dA,
+                                  float *dBm, float *dCm, float *dD_skip, float *dz,
+                                  float *ddelta_bias, float *d_init, void *workspace,
+                                  size_t workspace_bytes, void *stream);
+
+typedef enum kda_norm {
+  KDA_NORM_RMS = 0, /* x / sqrt(mean(x^2) + eps) */
+  KDA_NORM_L2 = 1   /* x / sqrt(sum(x^2) + eps): the unit rows kda_chunk_fwd takes */
+} kda_norm;
+
+typedef enum kda_rotation {
+  KDA_ROT_HALVES = 0, /* element i turns with element i + rot_dim / 2 */
+  KDA_ROT_PAIRS = 1   /* element 2 i turns with element 2 i + 1 */
+} kda_rotation;
+
+/*
+ * Norm of every query and key row (one head of one token) and the rotation
+ * of its first rot_dim elements by the token's position, in one pass:
+ *   u = x / sqrt(c sum(x^2) + eps) * weight,   c = 1/d (RMS) or 1 (L2),
+ *   pair i of u turns by the angle positions[token] * inv_freq[i].
+ *  q : in_dtype [tokens, Hq, d] rows, q_stride apart;  k : [tokens, Hk, d]
+ *  q_weight, k_weight : fp32 [d] or NULL (ones)
+ *  positions : int32 [tokens];  inv_freq : fp32 [rot_dim / 2]; both NULL with
+ *              rot_dim = 0 (no rotation).  The angle is formed and reduced
+ *              in fp64, so far positions keep their accuracy.
+ *  eps       : finite and > 0;  sum(x^2) has to be finite in fp32
+ *  q_out, k_out : in_dtype [tokens, Hq | Hk, d]; q_out may be q and k_out k
+ *              (in place, where the input is dense)
+ * Supported: d a multiple of 8 up to 256; rot_dim a multiple of 16 up to d.
+ */
+KDA_API kda_status kda_qk_norm_fwd(const void *q, int64_t q_stride, const void *k,
+                           int64_t k_stride, const float *q_weight, const float *k_weight,
+                           const int32_t *positions, const float *inv_freq,
+                           kda_dtype in_dtype, int tokens, int Hq, int Hk, int d, int rot_dim,
+                           kda_norm norm, kda_rotation rotation, float eps, void *q_out,
+                           void *k_out, void *stream);
+
+/*
+ * Gradients of kda_qk_norm_fwd.  With du the cotangent turned back and
+ * xh = x / sqrt(c sum(x^2) + eps):
+ *   dx = (du weight - xh c sum(du weight xh)) / sqrt(c sum(x^2) + eps),
+ *   dweight = sum over tokens and heads of du xh.
+ *  dq_out, dk_out : fp32 [tokens, Hq | Hk, d] (as kda_recurrent_bwd gives them)
+ *  dq, dk : fp32, same shapes; dq may be dq_out and dk may be dk_out
+ *  dq_weight, dk_weight : fp32 [d] or NULL (only with the weight given)
+ *  workspace : kda_qk_norm_bwd_workspace_size bytes (partial sums)
+ */
+KDA_API size_t kda_qk_norm_bwd_workspace_size(int tokens, int Hq, int Hk, int d);
+
+KDA_API kda_status kda_qk_norm_bwd(const void *q, int64_t q_stride, const void *k,
+                           int64_t k_stride, const float *q_weight, const float *k_weight,
+                           const int32_t *positions, const float *inv_freq,
+                           kda_dtype in_dtype, int tokens, int Hq, int Hk, int d, int rot_dim,
+                           kda_norm norm, kda_rotation rotation, float eps,
+                           const float *dq_out, const float *dk_out, float *dq, float *dk,
+                           float *dq_weight, float *dk_weight, void *workspace,
+                           size_t workspace_bytes, void *stream);
+
 /*
  * Name and description of the last CUDA error a libkda call on this host
  * thread turned into KDA_ERR_CUDA ("no error" if none).  Static storage.
