@@ -159,7 +159,8 @@ def _ptr(t):
 
 def _stream(stream):
     if stream is None:
-        return torch.cuda.current_stream().cuda_stream
+        # the handle alone: building a Stream object costs 3 us a call
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     if isinstance(stream, torch.cuda.Stream):
         return stream.cuda_stream
     return int(stream)
@@ -366,43 +367,49 @@ def kda_recurrent_bwd(q, k, v, g, beta, dout, grads, workspace, init_state=None,
 # ---- the operators around the recurrence: their inputs may be row slices of
 # wider tensors, so shapes, types and devices are checked here
 
-_F32T = (torch.float32,)
+# (tuples of types and shapes are compared as they are: these checks run on
+# every call of a decode loop)
+
+_F32T = torch.float32
 
 
-def _arg(name, t, shape, dtypes, optional=False):
+def _arg(dev, name, t, shape, dtype, optional=False):
     """The tensor's pointer, after checking that it is a dense CUDA tensor of
-    this shape and type on the current device."""
-    if t is None:
-        if optional:
-            return None
-        raise TypeError(f"{name}: expected a torch.Tensor")
-    _on_device(name, t, shape, dtypes)
+    this shape and type on device `dev`, the current one."""
+    if t is None and optional:
+        return None
+    _on_device(dev, name, t, shape, dtype)
     if not t.is_contiguous():
         raise ValueError(f"{name}: expected a dense tensor")
     return t.data_ptr()
 
 
-def _on_device(name, t, shape, dtypes):
+def _on_device(dev, name, t, shape, dtype):
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name}: expected a torch.Tensor")
-    if t.dtype not in dtypes:
-        raise TypeError(f"{name}: unsupported dtype {t.dtype}, expected {dtypes}")
-    if tuple(t.shape) != tuple(shape):
+    if t.dtype is not dtype:
+        raise TypeError(f"{name}: unsupported dtype {t.dtype}, expected {dtype}")
+    if t.shape != shape:
         raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)}")
-    if not t.is_cuda or t.device.index != torch.cuda.current_device():
+    if t.get_device() != dev:
         raise ValueError(f"{name}: expected a tensor on the current CUDA device")
 
 
 def _like(t):
-    """The types of a tensor that has to have t's element type."""
+    """The type of a tensor that has to have t's element type."""
     _dtype(t)
-    return (t.dtype,)
+    return t.dtype
 
 
-def _rows(name, t, shape, lead, dtypes):
+def _rows(dev, name, t, shape, lead, dtype):
     """(pointer, row stride) of a tensor whose first `lead` dimensions number
     its rows: rows dense, any constant distance apart."""
-    _on_device(name, t, shape, dtypes)
+    _on_device(dev, name, t, shape, dtype)
+    if t.is_contiguous():
+        width = 1
+        for n in shape[lead:]:
+            width *= n
+        return t.data_ptr(), width
     strides, width = t.stride(), 1
     for n, st in zip(reversed(shape[lead:]), reversed(strides[lead:])):
         if n > 1 and st != width:
@@ -425,22 +432,22 @@ def _rows(name, t, shape, lead, dtypes):
     return t.data_ptr(), stride
 
 
-def _grad(grads, name, shape, optional=False):
-    return _arg(f"grads['{name}']", grads.get(name), shape, _F32T, optional)
+def _grad(dev, grads, name, shape, optional=False):
+    return _arg(dev, f"grads['{name}']", grads.get(name), shape, _F32T, optional)
 
 
-def _offsets(cu_seqlens, batch):
+def _offsets(dev, cu_seqlens, batch):
     """(pointer, number of packed sequences, number of states)"""
     if cu_seqlens is None:
         return None, 0, batch
     n = cu_seqlens.numel() - 1
-    return _arg("cu_seqlens", cu_seqlens, (n + 1,), (torch.int32,)), n, n
+    return _arg(dev, "cu_seqlens", cu_seqlens, (n + 1,), torch.int32), n, n
 
 
-def _scratch(workspace):
+def _scratch(dev, workspace):
     if workspace is None:
         return None, 0
-    _on_device("workspace", workspace, workspace.shape, (workspace.dtype,))
+    _on_device(dev, "workspace", workspace, workspace.shape, workspace.dtype)
     return _ptr(workspace), workspace.numel() * workspace.element_size()
 
 
@@ -449,30 +456,32 @@ def kda_short_conv_fwd(x, weight, out, workspace, bias=None, init_state=None, cu
     """Causal convolution of each channel over its sequence's tokens; x [B,T,D]
     (rows may be slices of a wider tensor), weight fp32 [D,W], out [B,T,D],
     states [N,W-1,D] of x's type."""
+    dev = torch.cuda.current_device()
     B, T, D = x.shape
     W = weight.shape[-1]
     dt = _like(x)
-    cu, num, N = _offsets(cu_seqlens, B)
-    xp, xs = _rows("x", x, (B, T, D), 2, dt)
-    ws, wsb = _scratch(workspace)
+    cu, num, N = _offsets(dev, cu_seqlens, B)
+    xp, xs = _rows(dev, "x", x, (B, T, D), 2, dt)
+    ws, wsb = _scratch(dev, workspace)
     _check(lib().kda_short_conv_fwd(
-        xp, xs, _arg("weight", weight, (D, W), _F32T), _arg("bias", bias, (D,), _F32T, True),
-        _dtype(x), _arg("init_state", init_state, (N, W - 1, D), dt, True), cu, num, B, T, D, W,
-        int(activation), _arg("out", out, (B, T, D), dt),
-        _arg("final_state", final_state, (N, W - 1, D), dt, True), ws, wsb, _stream(stream)),
+        xp, xs, _arg(dev, "weight", weight, (D, W), _F32T), _arg(dev, "bias", bias, (D,), _F32T, True),
+        _dtype(x), _arg(dev, "init_state", init_state, (N, W - 1, D), dt, True), cu, num, B, T, D, W,
+        int(activation), _arg(dev, "out", out, (B, T, D), dt),
+        _arg(dev, "final_state", final_state, (N, W - 1, D), dt, True), ws, wsb, _stream(stream)),
         "kda_short_conv_fwd")
 
 
 def kda_short_conv_step(x, weight, state, out, bias=None, activation=KDA_ACT_SILU, stream=None):
     """One token of N sequences: x, out [N,D], state [N,W-1,D] shifted in place."""
+    dev = torch.cuda.current_device()
     N, D = x.shape
     W = weight.shape[-1]
     dt = _like(x)
-    xp, xs = _rows("x", x, (N, D), 1, dt)
+    xp, xs = _rows(dev, "x", x, (N, D), 1, dt)
     _check(lib().kda_short_conv_step(
-        xp, xs, _arg("weight", weight, (D, W), _F32T), _arg("bias", bias, (D,), _F32T, True),
-        _dtype(x), _arg("state", state, (N, W - 1, D), dt), N, D, W, int(activation),
-        _arg("out", out, (N, D), dt), _stream(stream)), "kda_short_conv_step")
+        xp, xs, _arg(dev, "weight", weight, (D, W), _F32T), _arg(dev, "bias", bias, (D,), _F32T, True),
+        _dtype(x), _arg(dev, "state", state, (N, W - 1, D), dt), N, D, W, int(activation),
+        _arg(dev, "out", out, (N, D), dt), _stream(stream)), "kda_short_conv_step")
 
 
 def kda_short_conv_bwd_workspace_size(B, T, D, W, num_seqs=0) -> int:
@@ -484,18 +493,19 @@ def kda_short_conv_bwd(x, weight, dout, grads, workspace, bias=None, init_state=
     """Gradients of kda_short_conv_fwd.  dout fp32 [B,T,D]; `grads` is a dict of
     fp32 outputs dx [B,T,D], dweight [D,W] and optionally dbias [D], d_init
     [N,W-1,D]."""
+    dev = torch.cuda.current_device()
     B, T, D = x.shape
     W = weight.shape[-1]
-    cu, num, N = _offsets(cu_seqlens, B)
-    xp, xs = _rows("x", x, (B, T, D), 2, _like(x))
-    ws, wsb = _scratch(workspace)
+    cu, num, N = _offsets(dev, cu_seqlens, B)
+    xp, xs = _rows(dev, "x", x, (B, T, D), 2, _like(x))
+    ws, wsb = _scratch(dev, workspace)
     _check(lib().kda_short_conv_bwd(
-        xp, xs, _arg("weight", weight, (D, W), _F32T), _arg("bias", bias, (D,), _F32T, True),
-        _dtype(x), _arg("init_state", init_state, (N, W - 1, D), (x.dtype,), True),
-        _arg("dout", dout, (B, T, D), _F32T),
-        _arg("d_final", d_final, (N, W - 1, D), _F32T, True), cu, num, B, T, D, W,
-        int(activation), _grad(grads, "dx", (B, T, D)), _grad(grads, "dweight", (D, W)),
-        _grad(grads, "dbias", (D,), True), _grad(grads, "d_init", (N, W - 1, D), True), ws, wsb,
+        xp, xs, _arg(dev, "weight", weight, (D, W), _F32T), _arg(dev, "bias", bias, (D,), _F32T, True),
+        _dtype(x), _arg(dev, "init_state", init_state, (N, W - 1, D), x.dtype, True),
+        _arg(dev, "dout", dout, (B, T, D), _F32T),
+        _arg(dev, "d_final", d_final, (N, W - 1, D), _F32T, True), cu, num, B, T, D, W,
+        int(activation), _grad(dev, grads, "dx", (B, T, D)), _grad(dev, grads, "dweight", (D, W)),
+        _grad(dev, grads, "dbias", (D,), True), _grad(dev, grads, "d_init", (N, W - 1, D), True), ws, wsb,
         _stream(stream)), "kda_short_conv_bwd")
 
 
@@ -503,16 +513,16 @@ def kda_selective_scan_fwd_workspace_size(B, T, D, S, G=1, num_seqs=0) -> int:
     return int(lib().kda_selective_scan_fwd_workspace_size(B, T, D, S, G, num_seqs))
 
 
-def _scan_inputs(x, delta, A, Bm, Cm, D, z, delta_bias, delta_softplus):
+def _scan_inputs(dev, x, delta, A, Bm, Cm, D, z, delta_bias, delta_softplus):
     """The marshalled input arguments that the scan's entries share."""
     lead, ch = tuple(x.shape[:-1]), x.shape[-1]
     S, G = A.shape[-1], Bm.shape[-2]
     n, dt = len(lead), _like(x)
-    args = [*_rows("x", x, (*lead, ch), n, dt), *_rows("delta", delta, (*lead, ch), n, dt),
-            _arg("A", A, (ch, S), _F32T), *_rows("Bm", Bm, (*lead, G, S), n, dt),
-            *_rows("Cm", Cm, (*lead, G, S), n, dt), _arg("D", D, (ch,), _F32T, True),
-            *((None, 0) if z is None else _rows("z", z, (*lead, ch), n, dt)),
-            _arg("delta_bias", delta_bias, (ch,), _F32T, True), int(bool(delta_softplus)),
+    args = [*_rows(dev, "x", x, (*lead, ch), n, dt), *_rows(dev, "delta", delta, (*lead, ch), n, dt),
+            _arg(dev, "A", A, (ch, S), _F32T), *_rows(dev, "Bm", Bm, (*lead, G, S), n, dt),
+            *_rows(dev, "Cm", Cm, (*lead, G, S), n, dt), _arg(dev, "D", D, (ch,), _F32T, True),
+            *((None, 0) if z is None else _rows(dev, "z", z, (*lead, ch), n, dt)),
+            _arg(dev, "delta_bias", delta_bias, (ch,), _F32T, True), int(bool(delta_softplus)),
             _dtype(x)]
     return args, ch, S, G
 
@@ -523,14 +533,15 @@ def kda_selective_scan_fwd(x, delta, A, Bm, Cm, out, workspace, D=None, z=None, 
     """Selective state space scan; x, delta, z, out [B,T,D], Bm, Cm [B,T,G,S]
     (inputs may be row slices of wider tensors), A fp32 [D,S], D and delta_bias
     fp32 [D], states fp32 [N,D,S]."""
+    dev = torch.cuda.current_device()
     B, T = x.shape[:2]
-    args, ch, S, G = _scan_inputs(x, delta, A, Bm, Cm, D, z, delta_bias, delta_softplus)
-    cu, num, N = _offsets(cu_seqlens, B)
-    ws, wsb = _scratch(workspace)
+    args, ch, S, G = _scan_inputs(dev, x, delta, A, Bm, Cm, D, z, delta_bias, delta_softplus)
+    cu, num, N = _offsets(dev, cu_seqlens, B)
+    ws, wsb = _scratch(dev, workspace)
     _check(lib().kda_selective_scan_fwd(
-        *args, _arg("init_state", init_state, (N, ch, S), _F32T, True), cu, num, B, T, ch, S, G,
-        _arg("out", out, (B, T, ch), (x.dtype,)),
-        _arg("final_state", final_state, (N, ch, S), _F32T, True), ws, wsb, _stream(stream)),
+        *args, _arg(dev, "init_state", init_state, (N, ch, S), _F32T, True), cu, num, B, T, ch, S, G,
+        _arg(dev, "out", out, (B, T, ch), x.dtype),
+        _arg(dev, "final_state", final_state, (N, ch, S), _F32T, True), ws, wsb, _stream(stream)),
         "kda_selective_scan_fwd")
 
 
@@ -538,11 +549,12 @@ def kda_selective_scan_step(x, delta, A, Bm, Cm, state, out, D=None, z=None, del
                             delta_softplus=True, stream=None):
     """One token of N sequences: x, delta, z, out [N,D], Bm, Cm [N,G,S], state
     fp32 [N,D,S] in place."""
+    dev = torch.cuda.current_device()
     N = x.shape[0]
-    args, ch, S, G = _scan_inputs(x, delta, A, Bm, Cm, D, z, delta_bias, delta_softplus)
+    args, ch, S, G = _scan_inputs(dev, x, delta, A, Bm, Cm, D, z, delta_bias, delta_softplus)
     _check(lib().kda_selective_scan_step(
-        *args, _arg("state", state, (N, ch, S), _F32T), N, ch, S, G,
-        _arg("out", out, (N, ch), (x.dtype,)), _stream(stream)), "kda_selective_scan_step")
+        *args, _arg(dev, "state", state, (N, ch, S), _F32T), N, ch, S, G,
+        _arg(dev, "out", out, (N, ch), x.dtype), _stream(stream)), "kda_selective_scan_step")
 
 
 def kda_selective_scan_bwd_workspace_size(B, T, D, S, G=1, num_seqs=0) -> int:
@@ -555,34 +567,35 @@ def kda_selective_scan_bwd(x, delta, A, Bm, Cm, dout, grads, workspace, D=None, 
     """Gradients of kda_selective_scan_fwd.  dout has x's type; `grads` is a
     dict of fp32 outputs dx, ddelta [B,T,D], dA [D,S], dB, dC [B,T,G,S], dz
     [B,T,D] with z, and optionally dD, ddelta_bias [D], d_init [N,D,S]."""
+    dev = torch.cuda.current_device()
     B, T = x.shape[:2]
-    args, ch, S, G = _scan_inputs(x, delta, A, Bm, Cm, D, z, delta_bias, delta_softplus)
-    cu, num, N = _offsets(cu_seqlens, B)
-    ws, wsb = _scratch(workspace)
+    args, ch, S, G = _scan_inputs(dev, x, delta, A, Bm, Cm, D, z, delta_bias, delta_softplus)
+    cu, num, N = _offsets(dev, cu_seqlens, B)
+    ws, wsb = _scratch(dev, workspace)
     _check(lib().kda_selective_scan_bwd(
-        *args, _arg("init_state", init_state, (N, ch, S), _F32T, True),
-        _arg("dout", dout, (B, T, ch), (x.dtype,)),
-        _arg("d_final", d_final, (N, ch, S), _F32T, True), cu, num, B, T, ch, S, G,
-        _grad(grads, "dx", (B, T, ch)), _grad(grads, "ddelta", (B, T, ch)),
-        _grad(grads, "dA", (ch, S)), _grad(grads, "dB", (B, T, G, S)),
-        _grad(grads, "dC", (B, T, G, S)), _grad(grads, "dD", (ch,), True),
-        _grad(grads, "dz", (B, T, ch), z is None), _grad(grads, "ddelta_bias", (ch,), True),
-        _grad(grads, "d_init", (N, ch, S), True), ws, wsb, _stream(stream)),
+        *args, _arg(dev, "init_state", init_state, (N, ch, S), _F32T, True),
+        _arg(dev, "dout", dout, (B, T, ch), x.dtype),
+        _arg(dev, "d_final", d_final, (N, ch, S), _F32T, True), cu, num, B, T, ch, S, G,
+        _grad(dev, grads, "dx", (B, T, ch)), _grad(dev, grads, "ddelta", (B, T, ch)),
+        _grad(dev, grads, "dA", (ch, S)), _grad(dev, grads, "dB", (B, T, G, S)),
+        _grad(dev, grads, "dC", (B, T, G, S)), _grad(dev, grads, "dD", (ch,), True),
+        _grad(dev, grads, "dz", (B, T, ch), z is None), _grad(dev, grads, "ddelta_bias", (ch,), True),
+        _grad(dev, grads, "d_init", (N, ch, S), True), ws, wsb, _stream(stream)),
         "kda_selective_scan_bwd")
 
 
-def _norm_inputs(q, k, q_weight, k_weight, positions, inv_freq, mode, rotation, eps):
+def _norm_inputs(dev, q, k, q_weight, k_weight, positions, inv_freq, mode, rotation, eps):
     lead, dim, dt = tuple(q.shape[:-2]), q.shape[-1], _like(q)
     Hq, Hk, n = q.shape[-2], k.shape[-2], len(lead)
     tokens = 1
     for m in lead:
         tokens *= m
     rot = 0 if inv_freq is None else 2 * inv_freq.numel()
-    args = [*_rows("q", q, (*lead, Hq, dim), n, dt), *_rows("k", k, (*lead, Hk, dim), n, dt),
-            _arg("q_weight", q_weight, (dim,), _F32T, True),
-            _arg("k_weight", k_weight, (dim,), _F32T, True),
-            _arg("positions", positions, lead, (torch.int32,), True),
-            _arg("inv_freq", inv_freq, (rot // 2,), _F32T, True), _dtype(q), tokens, Hq, Hk, dim,
+    args = [*_rows(dev, "q", q, (*lead, Hq, dim), n, dt), *_rows(dev, "k", k, (*lead, Hk, dim), n, dt),
+            _arg(dev, "q_weight", q_weight, (dim,), _F32T, True),
+            _arg(dev, "k_weight", k_weight, (dim,), _F32T, True),
+            _arg(dev, "positions", positions, lead, torch.int32, True),
+            _arg(dev, "inv_freq", inv_freq, (rot // 2,), _F32T, True), _dtype(q), tokens, Hq, Hk, dim,
             rot, int(mode), int(rotation), float(eps)]
     return args, lead, Hq, Hk, dim
 
@@ -594,11 +607,12 @@ def kda_qk_norm_fwd(q, k, q_out, k_out, q_weight=None, k_weight=None, positions=
     2 * inv_freq.numel() elements by positions [...] (int32) times inv_freq
     (fp32).  q [..., Hq, d], k [..., Hk, d] (rows of a token may be slices of
     a wider tensor); q_out, k_out dense, of the same type, or q, k themselves."""
-    args, lead, Hq, Hk, dim = _norm_inputs(q, k, q_weight, k_weight, positions, inv_freq, mode,
+    dev = torch.cuda.current_device()
+    args, lead, Hq, Hk, dim = _norm_inputs(dev, q, k, q_weight, k_weight, positions, inv_freq, mode,
                                            rotation, eps)
     _check(lib().kda_qk_norm_fwd(
-        *args, _arg("q_out", q_out, (*lead, Hq, dim), (q.dtype,)),
-        _arg("k_out", k_out, (*lead, Hk, dim), (q.dtype,)), _stream(stream)), "kda_qk_norm_fwd")
+        *args, _arg(dev, "q_out", q_out, (*lead, Hq, dim), q.dtype),
+        _arg(dev, "k_out", k_out, (*lead, Hk, dim), q.dtype), _stream(stream)), "kda_qk_norm_fwd")
 
 
 def kda_qk_norm_bwd_workspace_size(tokens, Hq, Hk, d) -> int:
@@ -611,14 +625,15 @@ def kda_qk_norm_bwd(q, k, dq_out, dk_out, grads, workspace=None, q_weight=None, 
     """Gradients of kda_qk_norm_fwd.  dq_out, dk_out fp32; `grads` is a dict of
     fp32 outputs dq, dk (dq may be dq_out itself, dk dk_out) and optionally
     dq_weight, dk_weight [d], which need the workspace."""
-    args, lead, Hq, Hk, dim = _norm_inputs(q, k, q_weight, k_weight, positions, inv_freq, mode,
+    dev = torch.cuda.current_device()
+    args, lead, Hq, Hk, dim = _norm_inputs(dev, q, k, q_weight, k_weight, positions, inv_freq, mode,
                                            rotation, eps)
-    ws, wsb = _scratch(workspace)
+    ws, wsb = _scratch(dev, workspace)
     _check(lib().kda_qk_norm_bwd(
-        *args, _arg("dq_out", dq_out, (*lead, Hq, dim), _F32T),
-        _arg("dk_out", dk_out, (*lead, Hk, dim), _F32T), _grad(grads, "dq", (*lead, Hq, dim)),
-        _grad(grads, "dk", (*lead, Hk, dim)), _grad(grads, "dq_weight", (dim,), True),
-        _grad(grads, "dk_weight", (dim,), True), ws, wsb, _stream(stream)), "kda_qk_norm_bwd")
+        *args, _arg(dev, "dq_out", dq_out, (*lead, Hq, dim), _F32T),
+        _arg(dev, "dk_out", dk_out, (*lead, Hk, dim), _F32T), _grad(dev, grads, "dq", (*lead, Hq, dim)),
+        _grad(dev, grads, "dk", (*lead, Hk, dim)), _grad(dev, grads, "dq_weight", (dim,), True),
+        _grad(dev, grads, "dk_weight", (dim,), True), ws, wsb, _stream(stream)), "kda_qk_norm_bwd")
 
 
 def kda_get_device_status(workspace, stream=None):

@@ -15,6 +15,7 @@ namespace {
 
 constexpr int kConvThreads = 256;
 constexpr int kUnroll = 8;  // rows in flight per thread
+constexpr int kFV = 4;      // channels per thread of the prompt kernel
 
 // ------------------------------------------------------------ packed batch
 __global__ void seqlens_plan_kernel(const int32_t* __restrict__ cu, int N, int T,
@@ -98,19 +99,18 @@ struct ConvArgs {
 
 // the run of tokens [t, end) of one sequence n that starts at `start`
 struct Run {
-  int n;
-  int64_t start, end;
+  int n, start, end;
 };
 
-__device__ __forceinline__ Run run_at(const ConvArgs& a, int64_t t) {
+__device__ __forceinline__ Run run_at(const ConvArgs& a, int t) {
   Run r;
   if (a.cu) {
-    r.n = find_range(a.cu, a.num_seqs, (int)t);
+    r.n = find_range(a.cu, a.num_seqs, t);
     r.start = __ldg(a.cu + r.n);
     r.end = __ldg(a.cu + r.n + 1);
   } else {
-    r.n = (int)(t / a.T);
-    r.start = (int64_t)r.n * a.T;
+    r.n = t / a.T;
+    r.start = r.n * a.T;
     r.end = r.start + a.T;
   }
   return r;
@@ -131,15 +131,15 @@ __device__ __forceinline__ void kept_row(const ConvArgs& a, int n, int back, int
 
 // win = the W - 1 rows before token t of run r, oldest first
 template <typename Tin, int W, int V>
-__device__ __forceinline__ void fill_window(const ConvArgs& a, const Run& r, int64_t t, int c,
+__device__ __forceinline__ void fill_window(const ConvArgs& a, const Run& r, int t, int c,
                                             float (&win)[W - 1][V]) {
 #pragma unroll
   for (int j = 0; j < W - 1; ++j) {
-    const int64_t s = t - (W - 1) + j;
+    const int s = t - (W - 1) + j;
     if (s >= r.start)
-      load_vec<Tin, V>(static_cast<const Tin*>(a.x) + s * a.x_stride + c, win[j]);
+      load_vec<Tin, V>(static_cast<const Tin*>(a.x) + (int64_t)s * a.x_stride + c, win[j]);
     else
-      kept_row<Tin, W, V>(a, r.n, (int)(r.start - s), c, win[j]);
+      kept_row<Tin, W, V>(a, r.n, r.start - s, c, win[j]);
   }
 }
 
@@ -156,12 +156,16 @@ __device__ __forceinline__ void push_row(float (&win)[W - 1][V], const float (&r
 template <int W, int V>
 __device__ __forceinline__ void load_taps(const ConvArgs& a, int c, float (&w)[V][W],
                                           float (&b)[V]) {
-  // V * W consecutive floats from a 16-byte boundary (c is a multiple of 4)
+  // V * W consecutive floats; c is a multiple of V, so V * W floats are a whole
+  // number of 8- or 16-byte pieces
   float flat[V * W];
+  constexpr int P = V * W % 4 == 0 ? 4 : 2;
 #pragma unroll
-  for (int i = 0; i < V * W; i += 4) {
-    const float4 f = __ldg(reinterpret_cast<const float4*>(a.weight + (int64_t)c * W + i));
-    flat[i] = f.x; flat[i + 1] = f.y; flat[i + 2] = f.z; flat[i + 3] = f.w;
+  for (int i = 0; i < V * W; i += P) {
+    float f[P];
+    load_vec<float, P>(a.weight + (int64_t)c * W + i, f);
+#pragma unroll
+    for (int j = 0; j < P; ++j) flat[i + j] = f[j];
   }
 #pragma unroll
   for (int i = 0; i < V; ++i)
@@ -214,11 +218,13 @@ __device__ __forceinline__ void store_final(const ConvArgs& a, int64_t item) {
 }
 
 // Threads [0, strips * D / V) take a strip each, channel groups fastest; the
-// blocks behind them write the final state.
+// blocks behind them write the final state.  Four channels a thread: eight
+// would double the window and tap registers and halve the warps in flight
+// (bf16 at W = 4: 506 us instead of KERNEL_US at 65,000 x 4096).
 template <typename Tin, int W>
-__global__ void __launch_bounds__(kConvThreads) conv_fwd_kernel(const ConvArgs a,
-                                                                unsigned strip_blocks) {
-  constexpr int V = 16 / sizeof(Tin);
+__global__ void __launch_bounds__(kConvThreads, 3) conv_fwd_kernel(const ConvArgs a,
+                                                                   unsigned strip_blocks) {
+  constexpr int V = kFV;
   if (a.cu) {
     if (!a.sb->seqlens_ok) return;
   } else if (blockIdx.x == 0 && threadIdx.x == 0) {
@@ -231,74 +237,95 @@ __global__ void __launch_bounds__(kConvThreads) conv_fwd_kernel(const ConvArgs a
   }
   const int CG = a.D / V;
   const int64_t idx = (int64_t)blockIdx.x * kConvThreads + threadIdx.x;
-  const int64_t strip = idx / CG;
+  const int strip = (int)(idx / CG);
   if (strip >= a.strips) return;
-  const int c = (int)(idx % CG) * V;
-  const int64_t t0 = strip * a.strip;
-  const int64_t t1 = min(t0 + a.strip, a.total);
-  const Tin* x = static_cast<const Tin*>(a.x);
-  Tin* out = static_cast<Tin*>(a.out);
+  const int c = (int)(idx - (int64_t)strip * CG) * V;
+  const int t0 = strip * a.strip;
+  const int t1 = (int)min((int64_t)t0 + a.strip, a.total);
+  const Tin* x = static_cast<const Tin*>(a.x) + (int64_t)t0 * a.x_stride + c;
+  Tin* out = static_cast<Tin*>(a.out) + (int64_t)t0 * a.D + c;
 
   float w[V][W], b[V], win[W - 1][V];
   load_taps<W, V>(a, c, w, b);
   Run r = run_at(a, t0);
   fill_window<Tin, W, V>(a, r, t0, c, win);
-  for (int64_t t = t0; t < t1; t += kUnroll) {
+  for (int t = t0; t < t1; t += kUnroll) {
     float row[kUnroll][V];
+    const bool whole = t + kUnroll <= t1 && t + kUnroll <= r.end;
+    if (whole) {
 #pragma unroll
-    for (int u = 0; u < kUnroll; ++u)
-      if (t + u < t1) load_vec<Tin, V>(x + (t + u) * a.x_stride + c, row[u]);
+      for (int u = 0; u < kUnroll; ++u) load_vec<Tin, V>(x + u * a.x_stride, row[u]);
 #pragma unroll
-    for (int u = 0; u < kUnroll; ++u) {
-      if (t + u < t1) {
-        if (t + u >= r.end) {  // the next sequence that has tokens
-          r = run_at(a, t + u);
-          fill_window<Tin, W, V>(a, r, t + u, c, win);
-        }
+      for (int u = 0; u < kUnroll; ++u) {
         float p[V];
         taps_dot<W, V>(w, b, win, row[u], p);
         if (a.silu) {
 #pragma unroll
           for (int i = 0; i < V; ++i) p[i] *= sigmoid_fast(p[i]);
         }
-        store_vec<V>(out + (t + u) * a.D + c, p);
+        store_vec<V>(out + (int64_t)u * a.D, p);
         push_row<W, V>(win, row[u]);
       }
+    } else {
+      for (int u = 0; u < kUnroll && t + u < t1; ++u) {
+        if (t + u >= r.end) {  // the next sequence that has tokens
+          r = run_at(a, t + u);
+          fill_window<Tin, W, V>(a, r, t + u, c, win);
+        }
+        float p[V];
+        load_vec<Tin, V>(x + u * a.x_stride, row[0]);
+        taps_dot<W, V>(w, b, win, row[0], p);
+        if (a.silu) {
+#pragma unroll
+          for (int i = 0; i < V; ++i) p[i] *= sigmoid_fast(p[i]);
+        }
+        store_vec<V>(out + (int64_t)u * a.D, p);
+        push_row<W, V>(win, row[0]);
+      }
     }
+    x += kUnroll * a.x_stride;
+    out += (int64_t)kUnroll * a.D;
   }
 }
 
-// One token of one sequence per thread and channel group; the state's rows
-// move one place up.
-template <typename Tin, int W>
+// One token of NS sequences per thread and channel group; the state's rows move
+// one place up.  The taps (16 bytes a channel) weigh as much as the rows, so
+// with enough sequences a thread keeps them for four.
+template <typename Tin, int W, int NS>
 __global__ void __launch_bounds__(kConvThreads)
-    conv_step_kernel(const Tin* __restrict__ x, int64_t x_stride,
-                     const float* __restrict__ weight, const float* __restrict__ bias,
-                     Tin* __restrict__ state, int N, int D, bool silu, Tin* __restrict__ out) {
-  constexpr int V = 16 / sizeof(Tin);
-  const int CG = D / V;
+    conv_step_kernel(const ConvArgs a, Tin* __restrict__ state, int N) {
+  constexpr int V = kFV;
+  const int CG = a.D / V;
   const int64_t idx = (int64_t)blockIdx.x * kConvThreads + threadIdx.x;
-  const int64_t n = idx / CG;
-  if (n >= N) return;
+  const int64_t n0 = idx / CG * NS;
+  if (n0 >= N) return;
   const int c = (int)(idx % CG) * V;
-  ConvArgs a{};
-  a.weight = weight;
-  a.bias = bias;
-  float win[W - 1][V], row[V], w[V][W], b[V], p[V];
-  Tin* st = state + n * (W - 1) * D + c;
-  load_vec<Tin, V>(x + n * x_stride + c, row);
+  float w[V][W], b[V];
+  float win[NS][W - 1][V], row[NS][V];
 #pragma unroll
-  for (int j = 0; j < W - 1; ++j) load_vec<Tin, V>(st + (int64_t)j * D, win[j]);
-  load_taps<W, V>(a, c, w, b);
-  taps_dot<W, V>(w, b, win, row, p);
-  if (silu) {
+  for (int s = 0; s < NS; ++s) {
+    if (n0 + s >= N) break;
+    load_vec<Tin, V>(static_cast<const Tin*>(a.x) + (n0 + s) * a.x_stride + c, row[s]);
 #pragma unroll
-    for (int i = 0; i < V; ++i) p[i] *= sigmoid_fast(p[i]);
+    for (int j = 0; j < W - 1; ++j)
+      load_vec<Tin, V>(state + ((n0 + s) * (W - 1) + j) * a.D + c, win[s][j]);
   }
-  store_vec<V>(out + n * D + c, p);
-  push_row<W, V>(win, row);
+  load_taps<W, V>(a, c, w, b);
 #pragma unroll
-  for (int j = 0; j < W - 1; ++j) store_vec<V>(st + (int64_t)j * D, win[j]);
+  for (int s = 0; s < NS; ++s) {
+    if (n0 + s >= N) break;
+    float p[V];
+    taps_dot<W, V>(w, b, win[s], row[s], p);
+    if (a.silu) {
+#pragma unroll
+      for (int i = 0; i < V; ++i) p[i] *= sigmoid_fast(p[i]);
+    }
+    store_vec<V>(static_cast<Tin*>(a.out) + (n0 + s) * a.D + c, p);
+    push_row<W, V>(win[s], row[s]);
+#pragma unroll
+    for (int j = 0; j < W - 1; ++j)
+      store_vec<V>(state + ((n0 + s) * (W - 1) + j) * a.D + c, win[s][j]);
+  }
 }
 
 // --------------------------------------------------------------- gradients
@@ -309,11 +336,12 @@ __global__ void __launch_bounds__(kConvThreads)
 // the last W - 1 values of ds stays in registers.  dweight and dbias are
 // summed in registers over the strip's own tokens and leave as one partial
 // row per strip, added in strip order by conv_bwd_sum_kernel.
-constexpr int kBV = 4;  // channels per thread: fp32 16-byte accesses
+constexpr int kBV = 2;  // channels per thread
+constexpr int kBU = 4;  // tokens whose rows are in flight
 
 template <typename Tin, int W>
-__global__ void __launch_bounds__(kConvThreads) conv_bwd_kernel(const ConvArgs a,
-                                                                unsigned strip_blocks) {
+__global__ void __launch_bounds__(kConvThreads, 3) conv_bwd_kernel(const ConvArgs a,
+                                                                   unsigned strip_blocks) {
   constexpr int V = kBV;
   if (a.cu) {
     if (!a.sb->seqlens_ok) return;
@@ -335,12 +363,11 @@ __global__ void __launch_bounds__(kConvThreads) conv_bwd_kernel(const ConvArgs a
     return;
   }
   const int64_t idx = (int64_t)blockIdx.x * kConvThreads + threadIdx.x;
-  const int64_t strip = idx / CG;
+  const int strip = (int)(idx / CG);
   if (strip >= a.strips) return;
-  const int c = (int)(idx % CG) * V;
-  const int64_t t0 = strip * a.strip;
-  const int64_t t1 = min(t0 + a.strip, a.total);
-  const Tin* x = static_cast<const Tin*>(a.x);
+  const int c = (int)(idx - (int64_t)strip * CG) * V;
+  const int t0 = strip * a.strip;
+  const int t1 = (int)min((int64_t)t0 + a.strip, a.total);
 
   float w[V][W], b[V], win[W - 1][V], dsw[W - 1][V], dw[V][W], db[V];
   load_taps<W, V>(a, c, w, b);
@@ -350,86 +377,97 @@ __global__ void __launch_bounds__(kConvThreads) conv_bwd_kernel(const ConvArgs a
 #pragma unroll
     for (int j = 0; j < W; ++j) dw[i][j] = 0.f;
   }
-  for (int64_t ta = t0; ta < t1;) {
+  for (int ta = t0; ta < t1;) {
     const Run r = run_at(a, ta);
-    const int64_t tb = min(t1, r.end);
+    const int tb = min(t1, r.end);
     fill_window<Tin, W, V>(a, r, ta, c, win);
 #pragma unroll
     for (int j = 0; j < W - 1; ++j)
 #pragma unroll
       for (int i = 0; i < V; ++i) dsw[j][i] = 0.f;
-    const bool head = ta == r.start;
-    constexpr int U = 4;  // tokens whose rows are in flight
-    for (int64_t tt = ta; tt < tb + W - 1; tt += U) {
-      float rows[U][V], dos[U][V];
+    const bool head = ta == r.start && a.d_init;
+    // token t's ds from its rows, its sums; then the gradient of row t - (W-1)
+    auto token = [&](int t, const float (&row)[V], const float (&dout)[V], bool own, bool give) {
+      float ds[V];
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const int64_t t = tt + u;
+      for (int i = 0; i < V; ++i) ds[i] = dout[i];
+      if (a.silu) {
+        float p[V];
+        taps_dot<W, V>(w, b, win, row, p);
 #pragma unroll
-        for (int i = 0; i < V; ++i) rows[u][i] = dos[u][i] = 0.f;
-        if (t < tb + W - 1 && t < r.end) {
-          load_vec<Tin, V>(x + t * a.x_stride + c, rows[u]);
-          load_vec<float, V>(a.dout + t * a.D + c, dos[u]);
+        for (int i = 0; i < V; ++i) {
+          const float sg = sigmoid_fast(p[i]);
+          ds[i] *= sg * fmaf(p[i], 1.f - sg, 1.f);
         }
       }
+      if (own) {
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const int64_t t = tt + u;
-        if (t >= tb + W - 1) continue;
-        float ds[V];
+        for (int i = 0; i < V; ++i) {
+          db[i] += ds[i];
 #pragma unroll
-        for (int i = 0; i < V; ++i) ds[i] = 0.f;
-        if (t < r.end) {
-          if (a.silu) {
-            float p[V];
-            taps_dot<W, V>(w, b, win, rows[u], p);
-#pragma unroll
-            for (int i = 0; i < V; ++i) {
-              const float sg = sigmoid_fast(p[i]);
-              ds[i] = dos[u][i] * (sg * fmaf(p[i], 1.f - sg, 1.f));
-            }
-          } else {
-#pragma unroll
-            for (int i = 0; i < V; ++i) ds[i] = dos[u][i];
-          }
-          if (t < tb) {
-#pragma unroll
-            for (int i = 0; i < V; ++i) {
-              db[i] += ds[i];
-#pragma unroll
-              for (int j = 0; j < W - 1; ++j) dw[i][j] = fmaf(ds[i], win[j][i], dw[i][j]);
-              dw[i][W - 1] = fmaf(ds[i], rows[u][i], dw[i][W - 1]);
-            }
-          }
-          push_row<W, V>(win, rows[u]);
+          for (int j = 0; j < W - 1; ++j) dw[i][j] = fmaf(ds[i], win[j][i], dw[i][j]);
+          dw[i][W - 1] = fmaf(ds[i], row[i], dw[i][W - 1]);
         }
-        const int64_t s = t - (W - 1);  // its gradient is complete
-        if (s >= ta || (head && a.d_init)) {
-          float g[V];
-#pragma unroll
-          for (int i = 0; i < V; ++i) {
-            g[i] = w[i][0] * ds[i];
-#pragma unroll
-            for (int j = 0; j < W - 1; ++j) g[i] = fmaf(w[i][W - 1 - j], dsw[j][i], g[i]);
-          }
-          const int64_t f = s - (r.end - (W - 1));  // its row of the final state
-          if (f >= 0 && a.d_final) {
-            float d[V];
-            load_vec<float, V>(a.d_final + ((int64_t)r.n * (W - 1) + f) * a.D + c, d);
-#pragma unroll
-            for (int i = 0; i < V; ++i) g[i] += d[i];
-          }
-          float* to = s >= ta ? a.dx + s * a.D
-                              : a.d_init + ((int64_t)r.n * (W - 1) + (s - ta + W - 1)) * a.D;
-          store_vec<V>(to + c, g);
-        }
-        push_row<W, V>(dsw, ds);
       }
+      push_row<W, V>(win, row);
+      if (give) {
+        float g[V];
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+          g[i] = w[i][0] * ds[i];
+#pragma unroll
+          for (int j = 0; j < W - 1; ++j) g[i] = fmaf(w[i][W - 1 - j], dsw[j][i], g[i]);
+        }
+        const int s = t - (W - 1);
+        const int f = s - (r.end - (W - 1));  // its row of the final state
+        if (f >= 0 && a.d_final) {
+          float d[V];
+          load_vec<float, V>(a.d_final + ((int64_t)r.n * (W - 1) + f) * a.D + c, d);
+#pragma unroll
+          for (int i = 0; i < V; ++i) g[i] += d[i];
+        }
+        float* to = s >= ta ? a.dx + (int64_t)s * a.D
+                            : a.d_init + ((int64_t)r.n * (W - 1) + (s - ta + W - 1)) * a.D;
+        store_vec<V>(to + c, g);
+      }
+      push_row<W, V>(dsw, ds);
+    };
+    const Tin* xp = static_cast<const Tin*>(a.x) + (int64_t)ta * a.x_stride + c;
+    const float* dp = a.dout + (int64_t)ta * a.D + c;
+    // the run's tokens, then the W - 1 behind them
+    for (int t = ta; t < tb; t += kBU) {
+      if (t >= ta + W - 1 && t + kBU <= tb) {
+        float rows[kBU][V], dos[kBU][V];
+#pragma unroll
+        for (int u = 0; u < kBU; ++u) {
+          load_vec<Tin, V>(xp + u * a.x_stride, rows[u]);
+          load_vec<float, V>(dp + (int64_t)u * a.D, dos[u]);
+        }
+#pragma unroll
+        for (int u = 0; u < kBU; ++u) token(t + u, rows[u], dos[u], true, true);
+      } else {
+        for (int u = 0; u < kBU && t + u < tb; ++u) {
+          float row[V], dout[V];
+          load_vec<Tin, V>(xp + u * a.x_stride, row);
+          load_vec<float, V>(dp + (int64_t)u * a.D, dout);
+          token(t + u, row, dout, true, head || t + u - (W - 1) >= ta);
+        }
+      }
+      xp += kBU * a.x_stride;
+      dp += (int64_t)kBU * a.D;
+    }
+    for (int t = tb; t < tb + W - 1; ++t) {
+      float row[V] = {}, dout[V] = {};
+      if (t < r.end) {
+        load_vec<Tin, V>(static_cast<const Tin*>(a.x) + (int64_t)t * a.x_stride + c, row);
+        load_vec<float, V>(a.dout + (int64_t)t * a.D + c, dout);
+      }
+      token(t, row, dout, false, head || t - (W - 1) >= ta);
     }
     ta = tb;
   }
   // [strip][W + 1][D]: tap j of all channels, then the bias
-  float* part = a.partial + strip * (W + 1) * a.D + c;
+  float* part = a.partial + (int64_t)strip * (W + 1) * a.D + c;
 #pragma unroll
   for (int j = 0; j < W; ++j) {
     float v[V];
@@ -485,7 +523,7 @@ int bwd_strip(int64_t total, int D) {
 
 template <typename Tin>
 cudaError_t dispatch_fwd(const ConvArgs& a, int W, cudaStream_t st) {
-  constexpr int V = 16 / sizeof(Tin);
+  constexpr int V = kFV;
   const int64_t blocks = ((int64_t)a.strips * (a.D / V) + kConvThreads - 1) / kConvThreads;
   int64_t fin = 0;
   if (a.final_state)
@@ -499,20 +537,30 @@ cudaError_t dispatch_fwd(const ConvArgs& a, int W, cudaStream_t st) {
   return cudaGetLastError();
 }
 
-template <typename Tin>
-cudaError_t dispatch_step(const void* x, int64_t xs, const float* w, const float* b, void* state,
-                          int N, int D, int W, bool silu, void* out, cudaStream_t st) {
-  constexpr int V = 16 / sizeof(Tin);
-  const unsigned grid = (unsigned)(((int64_t)N * (D / V) + kConvThreads - 1) / kConvThreads);
-  const Tin* xp = static_cast<const Tin*>(x);
+template <typename Tin, int W>
+cudaError_t launch_step(const ConvArgs& a, void* state, int N, cudaStream_t st) {
+  const int CG = a.D / kFV;
   Tin* sp = static_cast<Tin*>(state);
-  Tin* op = static_cast<Tin*>(out);
-  switch (W) {
-    case 2: conv_step_kernel<Tin, 2><<<grid, kConvThreads, 0, st>>>(xp, xs, w, b, sp, N, D, silu, op); break;
-    case 3: conv_step_kernel<Tin, 3><<<grid, kConvThreads, 0, st>>>(xp, xs, w, b, sp, N, D, silu, op); break;
-    default: conv_step_kernel<Tin, 4><<<grid, kConvThreads, 0, st>>>(xp, xs, w, b, sp, N, D, silu, op); break;
+  constexpr int NS = 4;
+  const int64_t few = ((int64_t)N + NS - 1) / NS * CG;  // threads with four sequences each
+  if (few >= kWantThreads / 2) {
+    conv_step_kernel<Tin, W, NS>
+        <<<(unsigned)((few + kConvThreads - 1) / kConvThreads), kConvThreads, 0, st>>>(a, sp, N);
+  } else {
+    const int64_t all = (int64_t)N * CG;
+    conv_step_kernel<Tin, W, 1>
+        <<<(unsigned)((all + kConvThreads - 1) / kConvThreads), kConvThreads, 0, st>>>(a, sp, N);
   }
   return cudaGetLastError();
+}
+
+template <typename Tin>
+cudaError_t dispatch_step(const ConvArgs& a, void* state, int N, int W, cudaStream_t st) {
+  switch (W) {
+    case 2: return launch_step<Tin, 2>(a, state, N, st);
+    case 3: return launch_step<Tin, 3>(a, state, N, st);
+    default: return launch_step<Tin, 4>(a, state, N, st);
+  }
 }
 
 template <typename Tin>
@@ -577,7 +625,7 @@ kda_status kda_short_conv_fwd(const void* x, int64_t x_stride, const float* weig
                        {workspace, (int64_t)kStatusBytes}};
   if (kda_status s = check_spans(ins, outs)) return s;
   if (workspace_bytes < kStatusBytes) return KDA_ERR_WORKSPACE;
-  const int V = (int)(16 / es);
+  const int V = kFV;
   ConvArgs a{};
   a.x = x;
   a.x_stride = x_stride;
@@ -618,20 +666,26 @@ kda_status kda_short_conv_step(const void* x, int64_t x_stride, const float* wei
                       {bias, (int64_t)D * 4}};
   const Span outs[] = {{out, (int64_t)N * D * es}, {state, (int64_t)N * (W - 1) * D * es}};
   if (kda_status s = check_spans(ins, outs)) return s;
-  if (!grid_fits((int64_t)N * (D / (16 / es)))) return KDA_ERR_UNSUPPORTED;
+  if (!grid_fits((int64_t)N * (D / kFV))) return KDA_ERR_UNSUPPORTED;
+  ConvArgs a{};
+  a.x = x;
+  a.x_stride = x_stride;
+  a.weight = weight;
+  a.bias = bias;
+  a.D = D;
+  a.silu = activation == KDA_ACT_SILU;
+  a.out = out;
   cudaStream_t st = (cudaStream_t)stream;
-  const bool silu = activation == KDA_ACT_SILU;
-  const cudaError_t e =
-      in_dtype == KDA_BF16
-          ? dispatch_step<__nv_bfloat16>(x, x_stride, weight, bias, state, N, D, W, silu, out, st)
-          : dispatch_step<float>(x, x_stride, weight, bias, state, N, D, W, silu, out, st);
+  const cudaError_t e = in_dtype == KDA_BF16
+                            ? dispatch_step<__nv_bfloat16>(a, state, N, W, st)
+                            : dispatch_step<float>(a, state, N, W, st);
   return e == cudaSuccess ? KDA_OK : cuda_failure(e);
 }
 
 size_t kda_short_conv_bwd_workspace_size(int B, int T, int D, int W, int num_seqs) {
   (void)num_seqs;
   if (B <= 0 || T <= 0 || D <= 0 || D % 8 != 0 || D > (1 << 24) || W < 2 || W > 4 ||
-      (int64_t)B * T > 0x7fffffffLL)
+      (int64_t)B * T > kMaxRows)
     return 0;
   const int64_t total = (int64_t)B * T;
   const int64_t strips = (total + bwd_strip(total, D) - 1) / bwd_strip(total, D);

@@ -64,10 +64,12 @@ __device__ __forceinline__ void fill_turns(const NormArgs& a, int t0, int nt, fl
 
 // Turns the 8 elements v of lane l (elements 8 l ..) by the table row `tab`;
 // sgn = 1 forward, -1 back.  All lanes of the warp take part.
-template <int L>
+enum Rot { kNoRot, kHalves, kPairs };
+
+template <int L, int ROT>
 __device__ __forceinline__ void turn(const NormArgs& a, const float2* tab, int l, float sgn,
                                      float (&v)[8]) {
-  if (a.pairs) {
+  if constexpr (ROT == kPairs) {
     if (8 * l < a.rot) {
 #pragma unroll
       for (int i = 0; i < 8; i += 2) {
@@ -77,18 +79,18 @@ __device__ __forceinline__ void turn(const NormArgs& a, const float2* tab, int l
         v[i + 1] = q * cs.x + p * s;
       }
     }
-    return;
-  }
-  const int hl = a.rot >> 4;  // lanes in half of the rotated part
-  const bool lo = l < hl, in = l < 2 * hl;
-  const int other = lo ? l + hl : l - hl;
-  const int src = in ? other : l;
+  } else if constexpr (ROT == kHalves) {
+    const int hl = a.rot >> 4;  // lanes in half of the rotated part
+    const bool lo = l < hl, in = l < 2 * hl;
+    const int src = in ? (lo ? l + hl : l - hl) : l;
+    const float2* row = tab + 8 * (lo ? l : l - hl);
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const float o = __shfl_sync(0xffffffffu, v[i], src, L);
-    if (in) {
-      const float2 cs = tab[8 * (lo ? l : other) + i];
-      v[i] = v[i] * cs.x + (lo ? -o : o) * (sgn * cs.y);
+    for (int i = 0; i < 8; ++i) {
+      const float o = __shfl_sync(0xffffffffu, v[i], src, L);
+      if (in) {
+        const float2 cs = row[i];
+        v[i] = v[i] * cs.x + (lo ? -o : o) * (sgn * cs.y);
+      }
     }
   }
 }
@@ -100,8 +102,33 @@ __device__ __forceinline__ float group_sum(float s) {
   return s;
 }
 
-template <typename Tin, int L>
-__global__ void __launch_bounds__(kNormThreads) qk_norm_fwd_kernel(const NormArgs a) {
+// A row of the block's tile: its token and where it lies.
+struct Row {
+  int tok, head;  // head of q, or of k from Hq on
+  bool isq;
+};
+
+__device__ __forceinline__ Row row_of(const NormArgs& a, int row, int H) {
+  Row r;
+  r.tok = a.per_block == 1 ? 0 : row / H;
+  r.head = row - r.tok * H;
+  r.isq = r.head < a.Hq;
+  return r;
+}
+
+template <typename Tin>
+__device__ __forceinline__ const Tin* in_row(const NormArgs& a, int64_t t, const Row& r) {
+  return r.isq ? static_cast<const Tin*>(a.q) + t * a.q_stride + r.head * a.d
+               : static_cast<const Tin*>(a.k) + t * a.k_stride + (r.head - a.Hq) * a.d;
+}
+
+// offset of a row of a dense q- or k-shaped tensor
+__device__ __forceinline__ int64_t dense_row(const NormArgs& a, int64_t t, const Row& r) {
+  return r.isq ? (t * a.Hq + r.head) * a.d : (t * a.Hk + r.head - a.Hq) * a.d;
+}
+
+template <typename Tin, int L, int ROT>
+__global__ void __launch_bounds__(kNormThreads, 4) qk_norm_fwd_kernel(const NormArgs a) {
   extern __shared__ float2 tab[];
   constexpr int G = kNormThreads / L;  // lane groups
   const int l = threadIdx.x % L, grp = threadIdx.x / L;
@@ -109,32 +136,19 @@ __global__ void __launch_bounds__(kNormThreads) qk_norm_fwd_kernel(const NormArg
   const int t0 = blockIdx.x * a.per_block;
   const int nt = min(a.per_block, a.tokens - t0);
   const int H = a.Hq + a.Hk, rows = nt * H;
-  float wq[8], wk[8];
-#pragma unroll
-  for (int i = 0; i < 8; ++i) wq[i] = wk[i] = 1.f;
-  if (act && a.q_weight) load_vec<float, 8>(a.q_weight + 8 * l, wq);
-  if (act && a.k_weight) load_vec<float, 8>(a.k_weight + 8 * l, wk);
-  bool filled = a.rot == 0;
+  bool filled = ROT == kNoRot;
   const int steps = (rows + G * kRowsInFlight - 1) / (G * kRowsInFlight);
   for (int s0 = 0; s0 < steps; ++s0) {
     float x[kRowsInFlight][8];
-    int tok[kRowsInFlight], head[kRowsInFlight];
+    Row r[kRowsInFlight];
 #pragma unroll
     for (int u = 0; u < kRowsInFlight; ++u) {
       const int row = (s0 * kRowsInFlight + u) * G + grp;
-      tok[u] = row / H;
-      head[u] = row - tok[u] * H;
+      r[u] = row_of(a, row, H);
 #pragma unroll
       for (int i = 0; i < 8; ++i) x[u][i] = 0.f;
-      if (row < rows && act) {
-        const int64_t t = t0 + tok[u];
-        if (head[u] < a.Hq)
-          load_vec<Tin, 8>(static_cast<const Tin*>(a.q) + t * a.q_stride +
-                               (int64_t)head[u] * a.d + 8 * l, x[u]);
-        else
-          load_vec<Tin, 8>(static_cast<const Tin*>(a.k) + t * a.k_stride +
-                               (int64_t)(head[u] - a.Hq) * a.d + 8 * l, x[u]);
-      }
+      if (row < rows && act)
+        load_vec<Tin, 8>(in_row<Tin>(a, t0 + r[u].tok, r[u]) + 8 * l, x[u]);
     }
     if (!filled) {
       fill_turns(a, t0, nt, tab);
@@ -147,20 +161,23 @@ __global__ void __launch_bounds__(kNormThreads) qk_norm_fwd_kernel(const NormArg
       float ss = 0.f;
 #pragma unroll
       for (int i = 0; i < 8; ++i) ss = fmaf(x[u][i], x[u][i], ss);
-      const float r = rsqrtf(fmaf(a.c, group_sum<L>(ss), a.eps));
-      const bool isq = head[u] < a.Hq;
+      const float f = rsqrtf(fmaf(a.c, group_sum<L>(ss), a.eps));
+      const float* wp = r[u].isq ? a.q_weight : a.k_weight;
+      if (wp && act) {
+        float w[8];
+        load_vec<float, 8>(wp + 8 * l, w);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) x[u][i] *= r * (isq ? wq[i] : wk[i]);
-      // rows past the end turn by the table's first token; nothing is stored
-      if (a.rot) turn<L>(a, tab + (row < rows ? tok[u] : 0) * (a.rot >> 1), l, 1.f, x[u]);
-      if (row < rows && act) {
-        const int64_t t = t0 + tok[u];
-        if (isq)
-          store_vec<8>(static_cast<Tin*>(a.q_out) + (t * a.Hq + head[u]) * a.d + 8 * l, x[u]);
-        else
-          store_vec<8>(static_cast<Tin*>(a.k_out) + (t * a.Hk + head[u] - a.Hq) * a.d + 8 * l,
-                       x[u]);
+        for (int i = 0; i < 8; ++i) x[u][i] *= f * w[i];
+      } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[u][i] *= f;
       }
+      // rows past the end turn by the table's first token; nothing is stored
+      if (ROT != kNoRot)
+        turn<L, ROT>(a, tab + (row < rows ? r[u].tok : 0) * (a.rot >> 1), l, 1.f, x[u]);
+      if (row < rows && act)
+        store_vec<8>(static_cast<Tin*>(r[u].isq ? a.q_out : a.k_out) +
+                         dense_row(a, t0 + r[u].tok, r[u]) + 8 * l, x[u]);
     }
   }
 }
@@ -168,53 +185,41 @@ __global__ void __launch_bounds__(kNormThreads) qk_norm_fwd_kernel(const NormArg
 // Blocks walk over token tiles; a lane's share of dweight (its 8 columns, the
 // rows of its group) stays in registers over the walk, is added over the
 // block's groups in order, and leaves as one partial row per block.
-template <typename Tin, int L>
-__global__ void __launch_bounds__(kNormThreads) qk_norm_bwd_kernel(const NormArgs a) {
+template <typename Tin, int L, int ROT>
+__global__ void __launch_bounds__(kNormThreads, 3) qk_norm_bwd_kernel(const NormArgs a) {
   extern __shared__ float2 tab[];
   constexpr int G = kNormThreads / L;
   constexpr int U = 2;
   const int l = threadIdx.x % L, grp = threadIdx.x / L;
   const bool act = 8 * l < a.d;
   const int H = a.Hq + a.Hk;
-  float wq[8], wk[8], gq[8], gk[8];
+  float gq[8], gk[8];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    wq[i] = wk[i] = 1.f;
-    gq[i] = gk[i] = 0.f;
-  }
-  if (act && a.q_weight) load_vec<float, 8>(a.q_weight + 8 * l, wq);
-  if (act && a.k_weight) load_vec<float, 8>(a.k_weight + 8 * l, wk);
+  for (int i = 0; i < 8; ++i) gq[i] = gk[i] = 0.f;
   for (int64_t t0 = (int64_t)blockIdx.x * a.per_block; t0 < a.tokens;
        t0 += (int64_t)a.blocks * a.per_block) {
     const int nt = (int)min((int64_t)a.per_block, a.tokens - t0);
     const int rows = nt * H;
     const int steps = (rows + G * U - 1) / (G * U);
-    if (a.rot) {
+    if (ROT != kNoRot) {
       __syncthreads();  // the last tile's table has been read
       fill_turns(a, (int)t0, nt, tab);
       __syncthreads();
     }
     for (int s0 = 0; s0 < steps; ++s0) {
       float x[U][8], dy[U][8];
-      int tok[U], head[U];
+      Row r[U];
 #pragma unroll
       for (int u = 0; u < U; ++u) {
         const int row = (s0 * U + u) * G + grp;
-        tok[u] = row / H;
-        head[u] = row - tok[u] * H;
+        r[u] = row_of(a, row, H);
 #pragma unroll
         for (int i = 0; i < 8; ++i) x[u][i] = dy[u][i] = 0.f;
         if (row < rows && act) {
-          const int64_t t = t0 + tok[u];
-          if (head[u] < a.Hq) {
-            load_vec<Tin, 8>(static_cast<const Tin*>(a.q) + t * a.q_stride +
-                                 (int64_t)head[u] * a.d + 8 * l, x[u]);
-            load_vec<float, 8>(a.dq_out + (t * a.Hq + head[u]) * a.d + 8 * l, dy[u]);
-          } else {
-            load_vec<Tin, 8>(static_cast<const Tin*>(a.k) + t * a.k_stride +
-                                 (int64_t)(head[u] - a.Hq) * a.d + 8 * l, x[u]);
-            load_vec<float, 8>(a.dk_out + (t * a.Hk + head[u] - a.Hq) * a.d + 8 * l, dy[u]);
-          }
+          const int64_t t = t0 + r[u].tok;
+          load_vec<Tin, 8>(in_row<Tin>(a, t, r[u]) + 8 * l, x[u]);
+          load_vec<float, 8>((r[u].isq ? a.dq_out : a.dk_out) + dense_row(a, t, r[u]) + 8 * l,
+                             dy[u]);
         }
       }
 #pragma unroll
@@ -223,29 +228,36 @@ __global__ void __launch_bounds__(kNormThreads) qk_norm_bwd_kernel(const NormArg
         float ss = 0.f;
 #pragma unroll
         for (int i = 0; i < 8; ++i) ss = fmaf(x[u][i], x[u][i], ss);
-        const float r = rsqrtf(fmaf(a.c, group_sum<L>(ss), a.eps));
-        const bool isq = head[u] < a.Hq;
-        if (a.rot) turn<L>(a, tab + (row < rows ? tok[u] : 0) * (a.rot >> 1), l, -1.f, dy[u]);
+        const float f = rsqrtf(fmaf(a.c, group_sum<L>(ss), a.eps));
+        if (ROT != kNoRot)
+          turn<L, ROT>(a, tab + (row < rows ? r[u].tok : 0) * (a.rot >> 1), l, -1.f, dy[u]);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[u][i] *= f;
+        if (a.partial) {  // rows past the end are zero
+          if (r[u].isq) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) gq[i] = fmaf(dy[u][i], x[u][i], gq[i]);
+          } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) gk[i] = fmaf(dy[u][i], x[u][i], gk[i]);
+          }
+        }
+        const float* wp = r[u].isq ? a.q_weight : a.k_weight;
+        if (wp && act) {
+          float w[8];
+          load_vec<float, 8>(wp + 8 * l, w);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) dy[u][i] *= w[i];
+        }
         float m = 0.f;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          x[u][i] *= r;
-          const float g = dy[u][i] * x[u][i];
-          if (isq) gq[i] += g;  // rows past the end are zero
-          else gk[i] += g;
-          dy[u][i] *= isq ? wq[i] : wk[i];
-          m = fmaf(dy[u][i], x[u][i], m);
-        }
+        for (int i = 0; i < 8; ++i) m = fmaf(dy[u][i], x[u][i], m);
         m = a.c * group_sum<L>(m);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) dy[u][i] = r * fmaf(-x[u][i], m, dy[u][i]);
-        if (row < rows && act) {
-          const int64_t t = t0 + tok[u];
-          if (isq)
-            store_vec<8>(a.dq + (t * a.Hq + head[u]) * a.d + 8 * l, dy[u]);
-          else
-            store_vec<8>(a.dk + (t * a.Hk + head[u] - a.Hq) * a.d + 8 * l, dy[u]);
-        }
+        for (int i = 0; i < 8; ++i) dy[u][i] = f * fmaf(-x[u][i], m, dy[u][i]);
+        if (row < rows && act)
+          store_vec<8>((r[u].isq ? a.dq : a.dk) + dense_row(a, t0 + r[u].tok, r[u]) + 8 * l,
+                       dy[u]);
       }
     }
   }
@@ -307,30 +319,42 @@ int bwd_blocks(int tokens, int H, int d) {
 
 size_t table_bytes(const NormArgs& a) { return sizeof(float2) * (size_t)a.per_block * (a.rot / 2); }
 
-template <typename Tin>
-cudaError_t dispatch_fwd(const NormArgs& a, cudaStream_t st) {
+template <typename Tin, int ROT>
+cudaError_t dispatch_fwd_rot(const NormArgs& a, cudaStream_t st) {
   const unsigned grid = (unsigned)(((int64_t)a.tokens + a.per_block - 1) / a.per_block);
   const size_t sm = table_bytes(a);
   switch (lane_group(a.d)) {
-    case 4: qk_norm_fwd_kernel<Tin, 4><<<grid, kNormThreads, sm, st>>>(a); break;
-    case 8: qk_norm_fwd_kernel<Tin, 8><<<grid, kNormThreads, sm, st>>>(a); break;
-    case 16: qk_norm_fwd_kernel<Tin, 16><<<grid, kNormThreads, sm, st>>>(a); break;
-    default: qk_norm_fwd_kernel<Tin, 32><<<grid, kNormThreads, sm, st>>>(a); break;
+    case 4: qk_norm_fwd_kernel<Tin, 4, ROT><<<grid, kNormThreads, sm, st>>>(a); break;
+    case 8: qk_norm_fwd_kernel<Tin, 8, ROT><<<grid, kNormThreads, sm, st>>>(a); break;
+    case 16: qk_norm_fwd_kernel<Tin, 16, ROT><<<grid, kNormThreads, sm, st>>>(a); break;
+    default: qk_norm_fwd_kernel<Tin, 32, ROT><<<grid, kNormThreads, sm, st>>>(a); break;
+  }
+  return cudaGetLastError();
+}
+
+template <typename Tin, int ROT>
+cudaError_t dispatch_bwd_rot(const NormArgs& a, cudaStream_t st) {
+  const size_t red = a.partial ? sizeof(float) * kNormThreads * 16 : 0;
+  const size_t sm = table_bytes(a) > red ? table_bytes(a) : red;
+  switch (lane_group(a.d)) {
+    case 4: qk_norm_bwd_kernel<Tin, 4, ROT><<<a.blocks, kNormThreads, sm, st>>>(a); break;
+    case 8: qk_norm_bwd_kernel<Tin, 8, ROT><<<a.blocks, kNormThreads, sm, st>>>(a); break;
+    case 16: qk_norm_bwd_kernel<Tin, 16, ROT><<<a.blocks, kNormThreads, sm, st>>>(a); break;
+    default: qk_norm_bwd_kernel<Tin, 32, ROT><<<a.blocks, kNormThreads, sm, st>>>(a); break;
   }
   return cudaGetLastError();
 }
 
 template <typename Tin>
+cudaError_t dispatch_fwd(const NormArgs& a, cudaStream_t st) {
+  if (a.rot == 0) return dispatch_fwd_rot<Tin, kNoRot>(a, st);
+  return a.pairs ? dispatch_fwd_rot<Tin, kPairs>(a, st) : dispatch_fwd_rot<Tin, kHalves>(a, st);
+}
+
+template <typename Tin>
 cudaError_t dispatch_bwd(const NormArgs& a, cudaStream_t st) {
-  const size_t red = a.partial ? sizeof(float) * kNormThreads * 16 : 0;
-  const size_t sm = table_bytes(a) > red ? table_bytes(a) : red;
-  switch (lane_group(a.d)) {
-    case 4: qk_norm_bwd_kernel<Tin, 4><<<a.blocks, kNormThreads, sm, st>>>(a); break;
-    case 8: qk_norm_bwd_kernel<Tin, 8><<<a.blocks, kNormThreads, sm, st>>>(a); break;
-    case 16: qk_norm_bwd_kernel<Tin, 16><<<a.blocks, kNormThreads, sm, st>>>(a); break;
-    default: qk_norm_bwd_kernel<Tin, 32><<<a.blocks, kNormThreads, sm, st>>>(a); break;
-  }
-  return cudaGetLastError();
+  if (a.rot == 0) return dispatch_bwd_rot<Tin, kNoRot>(a, st);
+  return a.pairs ? dispatch_bwd_rot<Tin, kPairs>(a, st) : dispatch_bwd_rot<Tin, kHalves>(a, st);
 }
 
 kda_status check_norm(const void* q, int64_t q_stride, const void* k, int64_t k_stride,

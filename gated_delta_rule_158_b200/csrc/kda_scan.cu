@@ -434,7 +434,7 @@ extern "C" {
 
 size_t kda_selective_scan_fwd_workspace_size(int B, int T, int D, int S, int G, int num_seqs) {
   if (B <= 0 || T <= 0 || D <= 0 || G <= 0 || num_seqs < 0 || !sizes_ok(D, S, G) ||
-      (int64_t)B * T > 0x7fffffffLL)
+      (int64_t)B * T > kMaxRows)
     return 0;
   static const int32_t packed = 0;  // only whether there are offsets matters here
   const Segments m = plan_segments(num_seqs > 0 && B == 1 ? &packed : nullptr, num_seqs, B, T, D, S);

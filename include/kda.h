@@ -410,7 +410,7 @@ typedef enum kda_activation { KDA_ACT_NONE = 0, KDA_ACT_SILU = 1 } kda_activatio
  *                later call or kda_short_conv_step continues from it
  *  workspace   : >= 256 bytes (the device status word, cleared by this call)
  * Arithmetic is fp32; out is rounded once.
- * Supported: W in {2, 3, 4}, D a multiple of 8, B * T < 2^31.
+ * Supported: W in {2, 3, 4}, D a multiple of 8, B * T <= 2^31 - 2^16.
  */
 KDA_API kda_status kda_short_conv_fwd(const void *x, int64_t x_stride, const float *weight,
                               const float *bias, kda_dtype in_dtype, const void *init_state,
@@ -471,7 +471,7 @@ KDA_API kda_status kda_short_conv_bwd(const void *x, int64_t x_stride, const flo
  * States and sums are fp32; out is rounded once.  A zero-length sequence has
  * final = init.
  * Supported: S in {8, 16, 32, 64, 128}; D a multiple of 8; G dividing D, with
- * D / G a multiple of 32 where G > 1; B * T < 2^31.
+ * D / G a multiple of 32 where G > 1; B * T <= 2^31 - 2^16.
  */
 KDA_API size_t kda_selective_scan_fwd_workspace_size(int B, int T, int D, int S, int G,
                                                      int num_seqs);

@@ -253,17 +253,17 @@ def test_binding_refuses_host_tensors_types_and_shapes(monkeypatch):
 def test_row_strides_of_slices(monkeypatch):
     monkeypatch.setattr(_lib, "_on_device", lambda *a: None)
     wide = torch.zeros(3, 5, 96)
-    f = (torch.float32,)
-    p, st = _lib._rows("x", wide[..., 32:64], (3, 5, 32), 2, f)
+    f = torch.float32
+    p, st = _lib._rows(0, "x", wide[..., 32:64], (3, 5, 32), 2, f)
     assert st == 96 and p == wide.data_ptr() + 32 * 4
-    assert _lib._rows("x", wide[:1, :1], (1, 1, 96), 2, f)[1] == 96  # no second row
-    assert _lib._rows("x", wide[:, 2:3], (3, 1, 96), 2, f)[1] == 480
-    assert _lib._rows("q", wide.view(3, 5, 4, 24)[:, :, 1:3], (3, 5, 2, 24), 2, f)[1] == 96
+    assert _lib._rows(0, "x", wide[:1, :1], (1, 1, 96), 2, f)[1] == 96  # no second row
+    assert _lib._rows(0, "x", wide[:, 2:3], (3, 1, 96), 2, f)[1] == 480
+    assert _lib._rows(0, "q", wide.view(3, 5, 4, 24)[:, :, 1:3], (3, 5, 2, 24), 2, f)[1] == 96
     with pytest.raises(ValueError, match="constant distance"):
-        _lib._rows("x", wide[:, :4], (3, 4, 96), 2, f)
+        _lib._rows(0, "x", wide[:, :4], (3, 4, 96), 2, f)
     with pytest.raises(ValueError, match="dense"):
-        _lib._rows("x", wide[..., ::2], (3, 5, 48), 2, f)
+        _lib._rows(0, "x", wide[..., ::2], (3, 5, 48), 2, f)
     with pytest.raises(ValueError, match="dense"):
-        _lib._rows("q", wide.view(3, 5, 4, 24)[:, :, ::2], (3, 5, 2, 24), 2, f)
+        _lib._rows(0, "q", wide.view(3, 5, 4, 24)[:, :, ::2], (3, 5, 2, 24), 2, f)
     with pytest.raises(ValueError):
-        _lib._rows("x", wide[:1, :1].expand(3, 5, 96), (3, 5, 96), 2, f)
+        _lib._rows(0, "x", wide[:1, :1].expand(3, 5, 96), (3, 5, 96), 2, f)
