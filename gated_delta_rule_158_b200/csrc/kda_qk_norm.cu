@@ -302,18 +302,25 @@ __global__ void __launch_bounds__(256) qk_norm_bwd_sum_kernel(const float* __res
 
 int lane_group(int d) { return d <= 32 ? 4 : d <= 64 ? 8 : d <= 128 ? 16 : 32; }
 
-// Tokens per block: enough rows for kRowsInFlight per lane group
-int tokens_per_block(int H, int d) {
+// Tokens per block: enough rows for kRowsInFlight per lane group; with a
+// rotation more, so that the block's threads form the angles of several tokens
+// at once (a token's 32 to 128 angles alone leave most of them waiting), as
+// long as every SM has four blocks.
+int tokens_per_block(int tokens, int H, int d, int rot) {
   const int groups = kNormThreads / lane_group(d);
   int n = groups * kRowsInFlight / H;
+  if (rot > 0) {
+    int m = 2 * kNormThreads / rot;
+    if (m > tokens / (148 * 4)) m = tokens / (148 * 4);
+    if (n < m) n = m;
+  }
   if (n > kMaxTokens) n = kMaxTokens;
   return n < 1 ? 1 : n;
 }
 
 constexpr int kBwdBlocks = 148 * 6;
-int bwd_blocks(int tokens, int H, int d) {
-  const int per = tokens_per_block(H, d);
-  const int64_t n = ((int64_t)tokens + per - 1) / per;
+int bwd_blocks(int tokens, int per_block) {
+  const int64_t n = ((int64_t)tokens + per_block - 1) / per_block;
   return (int)(n < kBwdBlocks ? n : kBwdBlocks);
 }
 
@@ -399,7 +406,7 @@ NormArgs norm_args(const void* q, int64_t q_stride, const void* k, int64_t k_str
   a.c = norm == KDA_NORM_RMS ? 1.0f / (float)d : 1.0f;
   a.eps = eps;
   a.pairs = rotation == KDA_ROT_PAIRS;
-  a.per_block = tokens_per_block(Hq + Hk, d);
+  a.per_block = tokens_per_block(tokens, Hq + Hk, d, rot_dim);
   return a;
 }
 
@@ -451,7 +458,8 @@ size_t kda_qk_norm_bwd_workspace_size(int tokens, int Hq, int Hk, int d) {
   if (tokens <= 0 || Hq <= 0 || Hk <= 0 || d <= 0 || d % 8 != 0 || d > 256 || Hq > (1 << 16) ||
       Hk > (1 << 16))
     return 0;
-  return sizeof(float) * (size_t)bwd_blocks(tokens, Hq + Hk, d) * 2 * d;
+  // without a rotation a block takes the fewest tokens
+  return sizeof(float) * (size_t)bwd_blocks(tokens, tokens_per_block(tokens, Hq + Hk, d, 0)) * 2 * d;
 }
 
 kda_status kda_qk_norm_bwd(const void* q, int64_t q_stride, const void* k, int64_t k_stride,
@@ -497,7 +505,7 @@ kda_status kda_qk_norm_bwd(const void* q, int64_t q_stride, const void* k, int64
   a.dq = dq;
   a.dk = dk;
   a.partial = sums ? static_cast<float*>(workspace) : nullptr;
-  a.blocks = bwd_blocks(tokens, Hq + Hk, d);
+  a.blocks = bwd_blocks(tokens, a.per_block);
   cudaStream_t st = (cudaStream_t)stream;
   cudaError_t e = in_dtype == KDA_BF16 ? dispatch_bwd<__nv_bfloat16>(a, st)
                                        : dispatch_bwd<float>(a, st);

@@ -2,6 +2,24 @@
 //
 //   h_t[d, s] = e^{dt A[d, s]} h_{t-1}[d, s] + dt x[t, d] B[t, s]
 //   y[t, d]   = sum_s C[t, s] h_t[d, s] + D[d] x[t, d],   out = y z sigmoid(z)
+//
+// An exponential per token, channel and state: the special-function unit (16
+// values a clock and SM) bounds it before HBM does (S = 16 states: 2 x 16 / 16
+// clocks against 4 x 2 bytes), and the registers that shared memory can fill
+// (128 bytes a clock and SM) are next: B and C of a token go to every thread.
+// So a thread has 4 states of SC channels: the token's 8 values of B and C
+// serve SC channels, its 2 SC values of dt and u = dt x serve 4 states.  With
+// two channels that is 12 words for 8 exponentials (three clocks of loads to
+// four of exponentials); with one, the loads are the bound, but a batch has
+// twice the warps.  Products over pairs of states take one instruction
+// (f32x2), and the sums over a channel's lanes are transposed over four tokens
+// (sum_lanes).
+//
+// A CTA has CT channels and walks its tokens in tiles of 32.  While a tile is
+// scanned the next one's x, dt, z, B and C are copied to slots of the shared
+// memory that only the copying thread reads (cp.async, no registers); each
+// thread then turns its own into the fp32 rows that the scan reads, token by
+// token.
 #include <math.h>
 
 #include "kda_scan.cuh"
@@ -10,34 +28,52 @@ namespace kda {
 namespace scan {
 namespace {
 
-constexpr int kTile = 32;            // tokens per tile
-constexpr int kPitch = kTile + 4;    // of a channel's row of a tile, in floats
+constexpr int kTile = 32;  // tokens per tile
 
-// position of token t in channel c's row of a tile: blocks of 4 or 8 tokens
-// change places by channel, so that the transposing stores (neighbouring lanes
-// hold neighbouring channel groups) spread over the banks
-template <int VEC>
-__device__ __forceinline__ int place(int c, int t) {
-  return VEC == 8 ? t ^ (((c >> 3) & 3) << 3) : t ^ (((c >> 2) & 7) << 2);
-}
+template <int S, int SC_>
+struct Layout {
+  static constexpr int SC = SC_;
+  static constexpr int LN = S / 4;                 // lanes of a channel
+  static constexpr int NT = LN <= 8 ? 128 : 256;
+  static constexpr int CT = SC * NT / LN;          // channels of a CTA
+  static constexpr int PER = kTile * CT / NT;      // elements of a tile per thread
+  static constexpr int VEC = PER > 4 ? 4 : PER < 2 ? 2 : PER;  // of them consecutive channels
+  static constexpr int ITEMS = PER < 2 ? 1 : PER / VEC, CV = CT / VEC;
+  static constexpr int BPT = kTile * S / NT > 4 ? 4 : kTile * S / NT;  // B, C elements per copy
+  static constexpr int BIT = kTile * S / NT / BPT;
+  static_assert(LN <= 32 && VEC >= SC, "layout");
+};
 
 // kOut: the outputs and the final state.  kEnd: only the state that the segment
-// leaves from a zero state, and its sum of dt (for all but a sequence's last
-// segment).  kEnds: those, and the state gradient that the segment's outputs
-// send to its start, sum_t (prod_{s <= t} e^{dt_s A}) C_t dy_t.
+// leaves and its sum of dt; kEnds: those, and the state gradient that the
+// segment's outputs send to its start, sum_t (prod_{s <= t} e^{dt_s A}) C_t dy_t.
 enum Mode { kOut, kEnd, kEnds };
 
-template <typename Tin, int S, int MODE>
-__global__ void __launch_bounds__(Layout<S>::NT) scan_fwd_kernel(const Args a) {
-  using L = Layout<S>;
-  constexpr int LN = L::LN, NT = L::NT, CT = L::CT;
-  constexpr int PER = kTile * CT / NT;             // elements of a tile per thread
-  constexpr int VEC = PER > 8 ? 8 : PER;           // of them consecutive channels
-  constexpr int ITEMS = PER / VEC, CV = CT / VEC;
-  constexpr int BPT = kTile * S / NT >= 4 ? 4 : kTile * S / NT;  // B, C elements per load
-  __shared__ __align__(16) float sdt[CT * kPitch], su[CT * kPitch];
-  __shared__ __align__(16) float sB[kTile * S], sC[MODE == kEnd ? 4 : kTile * S];
-  __shared__ __align__(16) float sdy[MODE == kEnds ? CT * kPitch : 4];
+template <typename Tin, int S, int SC, int MODE>
+struct Smem {
+  using L = Layout<S, SC>;
+  // fp32 rows of the tile, offsets in floats
+  static constexpr int kDu = 0;  // [token] store_du; behind the scan the outputs y
+  static constexpr int kDy = kDu + 2 * kTile * L::CT;
+  static constexpr int kB = kDy + (MODE == kEnds ? kTile * L::CT : 0);
+  static constexpr int kC = kB + kTile * S;
+  static constexpr int kRows = kC + (MODE == kEnd ? 0 : kTile * S);
+  // the threads' slots of two tiles: x, delta, z, dout; B, C
+  static constexpr int kArrays = MODE == kEnd ? 2 : MODE == kOut ? 3 : 4;
+  static constexpr int kItem = L::VEC * (int)sizeof(Tin), kBitem = L::BPT * (int)sizeof(Tin);
+  static constexpr int kSlots = L::NT * L::ITEMS * kItem * kArrays;  // bytes
+  static constexpr int kBslots = L::NT * L::BIT * kBitem * (MODE == kEnd ? 1 : 2);
+  static constexpr int kStage = kSlots + kBslots;
+  static constexpr size_t bytes() { return sizeof(float) * (size_t)kRows + 2 * (size_t)kStage; }
+};
+
+template <typename Tin, int S, int SC_, int MODE>
+__global__ void __launch_bounds__(Layout<S, SC_>::NT) scan_fwd_kernel(const Args a) {
+  using L = Layout<S, SC_>;
+  using M = Smem<Tin, S, SC_, MODE>;
+  constexpr int LN = L::LN, NT = L::NT, CT = L::CT, VEC = L::VEC, ITEMS = L::ITEMS, CV = L::CV,
+                BPT = L::BPT, BIT = L::BIT, SC = L::SC;
+  extern __shared__ __align__(16) float sm[];
 
   if (a.seg.cu) {
     if (!a.sb->seqlens_ok) return;
@@ -45,174 +81,279 @@ __global__ void __launch_bounds__(Layout<S>::NT) scan_fwd_kernel(const Args a) {
     a.sb->status = KDA_OK;
     a.sb->detail = 0;
   }
-  const int unit = blockIdx.x / a.nblk, cb = blockIdx.x % a.nblk;
-  const Unit un = resolve(a.seg, unit);
-  if (!un.valid || (MODE != kOut && un.last && (MODE == kEnd || un.first))) return;
-  const int tid = threadIdx.x, nl = tid % LN, c = tid / LN;
-  const int d0 = cb * CT, d = d0 + c;
-  const bool live = d < a.D;
-  const int g = d0 / (a.D / a.G);
-
-  float A2[4], h[4], prod[4], gs[4];
+  const int nblk = a.G * ((a.D / a.G + CT - 1) / CT);
+  const int ub = blockIdx.x / nblk;
+  const Unit un = resolve(a.seg, a.sb, ub);
+  // a sequence's last segment has no successor that needs its end state, its
+  // first none in front that needs its gradient; the checkpoints all do
+  if (!un.valid || (MODE != kOut && !a.ckpt && un.last && (MODE == kEnd || un.first))) return;
+  const int tid = threadIdx.x, nl = tid % LN, cp = tid / LN;
+  const Channels ch = channels_of<CT>(a, blockIdx.x - ub * nblk);
+  const int d = ch.d0 + SC * cp;
+  const bool live = SC * cp < ch.n;  // ch.n is a multiple of 8: both channels or none
+  const int64_t ds = (int64_t)a.D * S;
   const int64_t so = (int64_t)d * S + nl * 4;
+
+  float A2[SC][4];
+  f2 h[SC][2], prod[SC][2], gs[SC][2];
+  {
+    const float* from = MODE == kOut && a.h_seg ? a.h_seg + un.slot * ds
+                        : a.init && !(MODE != kOut && a.split) ? a.init + un.n * ds : nullptr;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    A2[i] = h[i] = gs[i] = 0.f;
-    prod[i] = 1.f;
-  }
-  if (live) {
-    load_vec<float, 4>(a.A + so, A2);
-    if (MODE == kOut) {
-      if (a.h_seg)
-        load_vec<float, 4>(a.h_seg + (int64_t)unit * a.D * S + so, h);
-      else if (a.init)
-        load_vec<float, 4>(a.init + (int64_t)un.n * a.D * S + so, h);
+    for (int q = 0; q < SC; ++q) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) A2[q][i] = 0.f;
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        h[q][i] = gs[q][i] = zero2();
+        prod[q][i] = pack2(1.f, 1.f);
+      }
+      if (live) {
+        load_vec<float, 4>(a.A + so + q * S, A2[q]);
+        if (from) load_pairs<2>(from + so + q * S, h[q]);
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) A2[q][i] *= kLog2e;
     }
   }
-#pragma unroll
-  for (int i = 0; i < 4; ++i) A2[i] *= kLog2e;
 
-  const int icv = tid % CV, it = tid / CV;  // the thread's channel group, first token
-  const int ic = icv * VEC;
-  const bool ilive = d0 + ic < a.D;  // D is a multiple of 8
-  float bias[VEC], skip[VEC], dsum[VEC];
+  // the thread's elements of a tile: tokens it + m NT / CV, channels ic ..
+  const int ic = tid % CV * VEC, it = tid / CV;
+  const bool item = it < kTile;
+  const bool ilive = item && ic < ch.n;
+  float dsum[VEC];
 #pragma unroll
-  for (int j = 0; j < VEC; ++j) bias[j] = skip[j] = dsum[j] = 0.f;
-  if (ilive && a.delta_bias) load_vec<float, VEC>(a.delta_bias + d0 + ic, bias);
-  if (ilive && a.D_skip) load_vec<float, VEC>(a.D_skip + d0 + ic, skip);
+  for (int j = 0; j < VEC; ++j) dsum[j] = 0.f;
 
-  for (int64_t t0 = un.t0; t0 < un.t1; t0 += kTile) {
-    float x[ITEMS][VEC];
+  const int len = (int)(un.t1 - un.t0);
+  const int tiles = (len + kTile - 1) / kTile;
+  const int64_t row0 = un.t0;
+  const int col = ch.d0 + ic;
+  char* const slots = reinterpret_cast<char*>(sm + M::kRows);
+  auto slot = [&](int i, int arr, int m) {
+    return slots + (i & 1) * M::kStage + ((arr * ITEMS + m) * NT + tid) * M::kItem;
+  };
+  auto bslot = [&](int i, int arr, int m) {
+    return slots + (i & 1) * M::kStage + M::kSlots + ((arr * BIT + m) * NT + tid) * M::kBitem;
+  };
+
+  auto copy_tile = [&](int i) {
+#pragma unroll
+    for (int m = 0; m < ITEMS; ++m) {
+      const int t = i * kTile + it + m * (NT / CV);
+      const bool in = ilive && t < len;
+      const int64_t row = in ? row0 + t : row0;
+      const int at = in ? col : 0;
+      copy_in<M::kItem>(slot(i, 0, m), static_cast<const Tin*>(a.x) + row * a.x_stride + at, in);
+      copy_in<M::kItem>(slot(i, 1, m), static_cast<const Tin*>(a.delta) + row * a.delta_stride + at,
+                        in);
+      if (MODE != kEnd && a.z)
+        copy_in<M::kItem>(slot(i, 2, m), static_cast<const Tin*>(a.z) + row * a.z_stride + at, in);
+      if (MODE == kEnds)
+        copy_in<M::kItem>(slot(i, 3, m), static_cast<const Tin*>(a.dout) + row * a.D + at, in);
+    }
+#pragma unroll
+    for (int m = 0; m < BIT; ++m) {
+      const int e = (tid + m * NT) * BPT, t = i * kTile + e / S;
+      const bool in = t < len;
+      const int64_t row = in ? row0 + t : row0;
+      const int at = ch.g * S + e % S;
+      copy_in<M::kBitem>(bslot(i, 0, m), static_cast<const Tin*>(a.Bm) + row * a.B_stride + at, in);
+      if (MODE != kEnd)
+        copy_in<M::kBitem>(bslot(i, 1, m), static_cast<const Tin*>(a.Cm) + row * a.C_stride + at,
+                           in);
+    }
+    copies_issued();
+  };
+  // the copied tile i as the rows that the scan reads
+  auto fill_tile = [&](int i) {
+    float bias[VEC] = {};
+    if (ilive && a.delta_bias) load_vec<float, VEC>(a.delta_bias + col, bias);
 #pragma unroll
     for (int m = 0; m < ITEMS; ++m) {
       const int t = it + m * (NT / CV);
-      float dt[VEC];
+      // a token behind the end leaves the state as it is: dt = 0
+      const bool in = ilive && i * kTile + t < len;
+      if (!item) continue;
+      float dt[VEC], u[VEC];
+      read_slot<Tin, VEC>(slot(i, 1, m), dt);
+      read_slot<Tin, VEC>(slot(i, 0, m), u);
 #pragma unroll
-      for (int j = 0; j < VEC; ++j) x[m][j] = dt[j] = 0.f;
-      if (ilive && t0 + t < un.t1) {
-        load_vec<Tin, VEC>(static_cast<const Tin*>(a.x) + (t0 + t) * a.x_stride + d0 + ic, x[m]);
-        load_vec<Tin, VEC>(static_cast<const Tin*>(a.delta) + (t0 + t) * a.delta_stride + d0 + ic,
-                           dt);
-#pragma unroll
-        for (int j = 0; j < VEC; ++j) dt[j] = step_size(dt[j] + bias[j], a.softplus);
-      }
-      if (MODE == kEnds) {
-        float dy[VEC];
-#pragma unroll
-        for (int j = 0; j < VEC; ++j) dy[j] = 0.f;
-        if (ilive && t0 + t < un.t1) {
-          load_vec<Tin, VEC>(static_cast<const Tin*>(a.dout) + (t0 + t) * a.D + d0 + ic, dy);
-          if (a.z) {
-            float zz[VEC];
-            load_vec<Tin, VEC>(static_cast<const Tin*>(a.z) + (t0 + t) * a.z_stride + d0 + ic, zz);
-#pragma unroll
-            for (int j = 0; j < VEC; ++j) dy[j] *= zz[j] * sigmoid_fast(zz[j]);
-          }
-        }
-#pragma unroll
-        for (int j = 0; j < VEC; ++j) sdy[(ic + j) * kPitch + place<VEC>(ic + j, t)] = dy[j];
-      }
+      for (int j = 0; j < VEC; ++j) dt[j] += bias[j];
+      step_sizes<VEC>(dt, a.softplus);
 #pragma unroll
       for (int j = 0; j < VEC; ++j) {
-        const int p = (ic + j) * kPitch + place<VEC>(ic + j, t);
-        sdt[p] = dt[j];
-        su[p] = dt[j] * x[m][j];
-        dsum[j] += dt[j];
+        dt[j] = in ? dt[j] : 0.f;
+        u[j] *= dt[j];
+        if (MODE != kOut) dsum[j] += dt[j];
+      }
+      store_du<SC, VEC>(sm + M::kDu + t * 2 * CT + 2 * ic, dt, u);
+      if (MODE == kEnds) {
+        float dy[VEC], z[VEC];
+        read_slot<Tin, VEC>(slot(i, 3, m), dy);
+        if (a.z) {
+          read_slot<Tin, VEC>(slot(i, 2, m), z);
+#pragma unroll
+          for (int j = 0; j < VEC; ++j) dy[j] *= z[j] * sigmoid2(z[j]);
+        }
+        store_vec<VEC>(sm + M::kDy + t * CT + ic, dy);
       }
     }
-    for (int e = tid * BPT; e < kTile * S; e += NT * BPT) {
-      const int t = e / S, s = e % S;
-      float b[BPT], cc[BPT];
 #pragma unroll
-      for (int j = 0; j < BPT; ++j) b[j] = cc[j] = 0.f;
-      if (t0 + t < un.t1) {
-        load_vec<Tin, BPT>(static_cast<const Tin*>(a.Bm) + (t0 + t) * a.B_stride + g * S + s, b);
-        if (MODE != kEnd)
-          load_vec<Tin, BPT>(static_cast<const Tin*>(a.Cm) + (t0 + t) * a.C_stride + g * S + s,
-                             cc);
-      }
-      store_vec<BPT>(sB + e, b);
-      if (MODE != kEnd) store_vec<BPT>(sC + e, cc);
-    }
-    __syncthreads();
-#pragma unroll 2
-    for (int t4 = 0; t4 < kTile; t4 += 4) {
-      const int p = c * kPitch + place<VEC>(c, t4);
-      const float4 dt4 = *reinterpret_cast<const float4*>(sdt + p);
-      const float4 u4 = *reinterpret_cast<const float4*>(su + p);
-      const float dts[4] = {dt4.x, dt4.y, dt4.z, dt4.w}, us[4] = {u4.x, u4.y, u4.z, u4.w};
-      float4 dy4 = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (MODE == kEnds) dy4 = *reinterpret_cast<const float4*>(sdy + p);
-      const float dys[4] = {dy4.x, dy4.y, dy4.z, dy4.w};
-      float y[4];
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const float4 b4 = *reinterpret_cast<const float4*>(sB + (t4 + k) * S + nl * 4);
-        const float bs[4] = {b4.x, b4.y, b4.z, b4.w};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float w = ex2(dts[k] * A2[i]);
-          h[i] = fmaf(w, h[i], us[k] * bs[i]);
-          if (MODE == kEnds) prod[i] *= w;
-        }
-        if (MODE == kEnds) {
-          const float4 c4 = *reinterpret_cast<const float4*>(sC + (t4 + k) * S + nl * 4);
-          const float cs[4] = {c4.x, c4.y, c4.z, c4.w};
-#pragma unroll
-          for (int i = 0; i < 4; ++i) gs[i] = fmaf(prod[i] * cs[i], dys[k], gs[i]);
-        }
-        if (MODE == kOut) {
-          const float4 c4 = *reinterpret_cast<const float4*>(sC + (t4 + k) * S + nl * 4);
-          y[k] = fmaf(c4.x, h[0], c4.y * h[1]) + fmaf(c4.z, h[2], c4.w * h[3]);
-        }
-      }
-      if (MODE == kOut) {
-        // the channel's lanes have read their u: y takes its place
-        const float2 r = sum_lanes<LN>(y, nl);
-        if (LN == 2)
-          *reinterpret_cast<float2*>(su + p + 2 * nl) = r;
-        else if (nl < 4)
-          su[p + nl] = r.x;
+    for (int m = 0; m < BIT; ++m) {
+      const int e = (tid + m * NT) * BPT;
+      float b[BPT];
+      read_slot<Tin, BPT>(bslot(i, 0, m), b);
+      store_vec<BPT>(sm + M::kB + e, b);
+      if (MODE != kEnd) {
+        read_slot<Tin, BPT>(bslot(i, 1, m), b);
+        store_vec<BPT>(sm + M::kC + e, b);
       }
     }
-    __syncthreads();
-    if (MODE == kOut) {
+  };
+  float cum[SC];  // sum of dt in front of the tile's tokens (checkpoints)
 #pragma unroll
-      for (int m = 0; m < ITEMS; ++m) {
-        const int t = it + m * (NT / CV);
-        if (ilive && t0 + t < un.t1) {
-          float y[VEC];
+  for (int q = 0; q < SC; ++q) cum[q] = 0.f;
+  const int64_t tile0 = first_tile(un);
+  // Two tokens' operands, loaded and their decays formed while the two tokens
+  // before are applied: a store to shared memory keeps the compiler from moving
+  // later loads in front of it, and a warp alone on its scheduler would wait
+  // for every load and exponential.
+  struct Pair {
+    f2 w[2][SC][2], b[2][2], c[2][2];
+    float dt[2][SC], u[2][SC], dy[2][SC];
+  };
+  float* pdu = sm + M::kDu + 2 * SC * cp;
+  const float* pdy = sm + M::kDy + SC * cp;
+  const float* pb = sm + M::kB + nl * 4;
+  const float* pc = sm + M::kC + nl * 4;
+  auto fetch = [&](Pair& g, int t) {
 #pragma unroll
-          for (int j = 0; j < VEC; ++j)
-            y[j] = fmaf(skip[j], x[m][j], su[(ic + j) * kPitch + place<VEC>(ic + j, t)]);
-          if (a.z) {
-            float zz[VEC];
-            load_vec<Tin, VEC>(static_cast<const Tin*>(a.z) + (t0 + t) * a.z_stride + d0 + ic, zz);
+    for (int k = 0; k < 2; ++k) {
+      load_du<SC>(pdu + (t + k) * 2 * CT, g.dt[k], g.u[k]);
+      load_pairs<2>(pb + (t + k) * S, g.b[k]);
+      if (MODE != kEnd) load_pairs<2>(pc + (t + k) * S, g.c[k]);
+      if (MODE == kEnds) load_vec<float, SC>(pdy + (t + k) * CT, g.dy[k]);
+    }
+  };
+  auto decays = [&](Pair& g) {
 #pragma unroll
-            for (int j = 0; j < VEC; ++j) y[j] *= zz[j] * sigmoid_fast(zz[j]);
+    for (int k = 0; k < 2; ++k)
+#pragma unroll
+      for (int q = 0; q < SC; ++q)
+#pragma unroll
+        for (int p = 0; p < 2; ++p)
+          g.w[k][q][p] = pack2(ex2(g.dt[k][q] * A2[q][2 * p]), ex2(g.dt[k][q] * A2[q][2 * p + 1]));
+  };
+  auto apply = [&](const Pair& g, float (&y)[SC][4], int at) {
+#pragma unroll
+    for (int k = 0; k < 2; ++k)
+#pragma unroll
+      for (int q = 0; q < SC; ++q) {
+        const f2 uu = pack2(g.u[k][q], g.u[k][q]);
+        f2 yy;
+#pragma unroll
+        for (int p = 0; p < 2; ++p) {
+          h[q][p] = fma2(g.w[k][q][p], h[q][p], mul2(uu, g.b[k][p]));
+          if (MODE == kOut) yy = p == 0 ? mul2(g.c[k][0], h[q][0]) : fma2(g.c[k][p], h[q][p], yy);
+          if (MODE == kEnds) {
+            prod[q][p] = mul2(prod[q][p], g.w[k][q][p]);
+            gs[q][p] = fma2(mul2(prod[q][p], g.c[k][p]), pack2(g.dy[k][q], g.dy[k][q]), gs[q][p]);
           }
-          store_vec<VEC>(static_cast<Tin*>(a.out) + (t0 + t) * a.D + d0 + ic, y);
         }
+        if (MODE == kOut) y[q][at + k] = sum2(yy);
+        else cum[q] += g.dt[k][q];
       }
-      __syncthreads();  // su is written again
+  };
+  auto keep = [&](int t) {  // the states in front of the segment's token t
+    if (a.ckpt && t < len && live) {
+      const int64_t at = tile0 + t / kStep;
+#pragma unroll
+      for (int q = 0; q < SC; ++q) {
+        store_pairs<2>(a.ckpt + at * ds + so + q * S, h[q]);
+        if (a.split && nl == 0) a.ckpt_dt[at * a.D + d + q] = cum[q];
+      }
     }
+  };
+  auto scan_tile = [&](int i) {
+    Pair g0, g1;
+    fetch(g0, 0);
+    decays(g0);
+#pragma unroll 1
+    for (int t8 = 0; t8 < kTile; t8 += 8) {
+      if (MODE != kOut) keep(i * kTile + t8);
+#pragma unroll
+      for (int t4 = t8; t4 < t8 + 8; t4 += 4) {
+        float y[SC][4];
+        fetch(g1, t4 + 2);
+        apply(g0, y, 0);
+        decays(g1);
+        // behind the last tokens their own rows again, unused
+        fetch(g0, t4 + 4 < kTile ? t4 + 4 : t4 + 2);
+        apply(g1, y, 2);
+        decays(g0);
+        // y takes the place of the four tokens' dt: only the channel's lanes, all
+        // of them in this warp, read it, and they have
+        if (MODE == kOut) store_sums<SC, LN, 2 * CT>(pdu + t4 * 2 * CT, y, nl);
+      }
+    }
+  };
+  auto store_tile = [&](int i) {
+    float skip[VEC] = {};
+    if (ilive && a.D_skip) load_vec<float, VEC>(a.D_skip + col, skip);
+#pragma unroll
+    for (int m = 0; m < ITEMS; ++m) {
+      const int t = it + m * (NT / CV);
+      if (ilive && i * kTile + t < len) {
+        float y[VEC], x[VEC], z[VEC];
+        read_slot<Tin, VEC>(slot(i, 0, m), x);
+        if (a.z) read_slot<Tin, VEC>(slot(i, 2, m), z);
+        load_sums<SC, VEC>(sm + M::kDu + t * 2 * CT + 2 * ic, y);
+#pragma unroll
+        for (int j = 0; j < VEC; ++j) {
+          y[j] = fmaf(skip[j], x[j], y[j]);
+          if (a.z) y[j] *= z[j] * sigmoid2(z[j]);
+        }
+        store_vec<VEC>(static_cast<Tin*>(a.out) + (row0 + i * kTile + t) * a.D + col, y);
+      }
+    }
+  };
+
+  if (tiles > 0) copy_tile(0);
+  for (int i = 0; i < tiles; ++i) {
+    copies_landed();  // this thread's own: nobody else reads its slots
+    fill_tile(i);
+    __syncthreads();
+    if (i + 1 < tiles) copy_tile(i + 1);
+    scan_tile(i);
+    __syncthreads();
+    if (MODE == kOut) store_tile(i);
   }
   if (MODE != kOut) {
-    if (live) store_vec<4>(a.h_seg + (int64_t)unit * a.D * S + so, h);
-    if (MODE == kEnds && live) store_vec<4>(a.g_seg + (int64_t)unit * a.D * S + so, gs);
-    // dt summed over the threads that share a channel group, in order
-    float* red = su;
-    __syncthreads();
+    if (!a.split) return;  // the checkpoints alone were wanted
+    if (live) {
 #pragma unroll
-    for (int j = 0; j < VEC; ++j) red[it * CT + ic + j] = dsum[j];
+      for (int q = 0; q < SC; ++q) {
+        store_pairs<2>(a.h_seg + un.slot * ds + so + q * S, h[q]);
+        if (MODE == kEnds) store_pairs<2>(a.g_seg + un.slot * ds + so + q * S, gs[q]);
+      }
+    }
+    // dt summed over the threads that share a channel group, in order
+    float* red = sm;
+    if (item) {
+#pragma unroll
+      for (int j = 0; j < VEC; ++j) red[it * CT + ic + j] = dsum[j];
+    }
     __syncthreads();
-    if (tid < CT && d0 + tid < a.D) {
+    constexpr int ROWS = NT / CV < kTile ? NT / CV : kTile;
+    for (int e = tid; e < ch.n; e += NT) {
       float s = 0.f;
-      for (int r = 0; r < NT / CV; ++r) s += red[r * CT + tid];
-      a.dt_sum[(int64_t)unit * a.D + d0 + tid] = s;
+      for (int r = 0; r < ROWS; ++r) s += red[r * CT + e];
+      a.dt_sum[(int64_t)un.slot * a.D + ch.d0 + e] = s;
     }
   } else if (un.last && a.final_state && live) {
-    store_vec<4>(a.final_state + (int64_t)un.n * a.D * S + so, h);
+#pragma unroll
+    for (int q = 0; q < SC; ++q) store_pairs<2>(a.final_state + un.n * ds + so + q * S, h[q]);
   }
 }
 
@@ -234,89 +375,238 @@ __global__ void __launch_bounds__(256) scan_combine_kernel(const Args a) {
   float A[4], in[4] = {};
   load_vec<float, 4>(a.A + e, A);
   if (a.init) load_vec<float, 4>(a.init + n * ds + e, in);
-  for (int u = u0; u < u1; ++u) {
-    float* at = a.h_seg + u * ds + e;
-    float own[4] = {}, w = 0.f;
-    if (u + 1 < u1) {
-      load_vec<float, 4>(at, own);
-      w = a.dt_sum[(int64_t)u * a.D + d];
-    }
-    store_vec<4>(at, in);
+  // eight segments' values in flight: the chain itself is a multiply-add each
+  constexpr int U = 8;
+  for (int ua = u0; ua < u1; ua += U) {
+    float own[U][4], w[U];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) in[i] = fmaf(ex2(w * (A[i] * kLog2e)), in[i], own[i]);
+    for (int k = 0; k < U; ++k) {
+      w[k] = own[k][0] = own[k][1] = own[k][2] = own[k][3] = 0.f;
+      if (ua + k + 1 < u1) {
+        load_vec<float, 4>(a.h_seg + (ua + k) * ds + e, own[k]);
+        w[k] = a.dt_sum[(int64_t)(ua + k) * a.D + d];
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < U; ++k) {
+      if (ua + k >= u1) break;
+      store_vec<4>(a.h_seg + (ua + k) * ds + e, in);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) in[i] = fmaf(ex2(w[k] * (A[i] * kLog2e)), in[i], own[k][i]);
+    }
   }
   if (!a.g_seg) return;
 #pragma unroll
   for (int i = 0; i < 4; ++i) in[i] = 0.f;
   if (a.d_final) load_vec<float, 4>(a.d_final + n * ds + e, in);
-  for (int u = u1 - 1; u >= u0; --u) {
-    float* at = a.g_seg + u * ds + e;
-    float own[4] = {}, w = 0.f;
-    if (u > u0) {
-      load_vec<float, 4>(at, own);
-      w = a.dt_sum[(int64_t)u * a.D + d];
-    }
-    store_vec<4>(at, in);
+  for (int ua = u1 - 1; ua >= u0; ua -= U) {
+    float own[U][4], w[U];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) in[i] = fmaf(ex2(w * (A[i] * kLog2e)), in[i], own[i]);
+    for (int k = 0; k < U; ++k) {
+      w[k] = own[k][0] = own[k][1] = own[k][2] = own[k][3] = 0.f;
+      if (ua - k > u0) {
+        load_vec<float, 4>(a.g_seg + (ua - k) * ds + e, own[k]);
+        w[k] = a.dt_sum[(int64_t)(ua - k) * a.D + d];
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < U; ++k) {
+      if (ua - k < u0) break;
+      store_vec<4>(a.g_seg + (ua - k) * ds + e, in);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) in[i] = fmaf(ex2(w[k] * (A[i] * kLog2e)), in[i], own[k][i]);
+    }
   }
 }
 
-// One token: a thread has 4 states of a channel of a sequence.  HBM-bound: the
-// fp32 states are read once and written once.
-template <typename Tin, int S>
+// One token: a thread has 4 states of a channel, of NSEQ sequences.  HBM-bound:
+// the fp32 states are read once and written once; A, as large as one
+// sequence's states, is kept for the NSEQ sequences.  Lane k of a channel's
+// lanes forms dt and u of sequence k for all of them, and receives its sum y
+// (transposed over the sequences), so what is per channel is done once.
+template <typename Tin, int S, int NSEQ>
 __global__ void __launch_bounds__(256) scan_step_kernel(const Args a, float* state, int N) {
   constexpr int LN = S / 4;
+  static_assert(NSEQ == 1 || (NSEQ == 4 && LN >= 4), "lanes per channel");
   const int64_t idx = (int64_t)blockIdx.x * 256 + threadIdx.x;
   const int nl = (int)(idx % LN);
   const int64_t cn = idx / LN;
-  const int64_t n = cn / a.D;
-  const bool live = n < N;  // LN divides 32: a channel's lanes share this
-  const int d = (int)(cn % a.D);
-  float y = 0.f, x = 0.f;
-  if (live) {
-    const int g = d / (a.D / a.G);
-    float h[4], A[4], b[4], c[4];
-    float* st = state + (n * a.D + d) * S + nl * 4;
-    load_vec<float, 4>(st, h);
-    load_vec<float, 4>(a.A + (int64_t)d * S + nl * 4, A);
-    load_vec<Tin, 4>(static_cast<const Tin*>(a.Bm) + n * a.B_stride + g * S + nl * 4, b);
-    load_vec<Tin, 4>(static_cast<const Tin*>(a.Cm) + n * a.C_stride + g * S + nl * 4, c);
+  const int64_t n0 = cn / a.D * NSEQ;
+  const int d = (int)(cn - n0 / NSEQ * a.D);
+  const int ns = n0 < N ? (int)min((int64_t)NSEQ, N - n0) : 0;
+  const int g = d / (a.D / a.G);
+  const int64_t so = (int64_t)d * S + nl * 4, ds = (int64_t)a.D * S;
+  float A2[4] = {};
+  f2 h[NSEQ][2];
+  Raw<Tin, 4> b[NSEQ], c[NSEQ];
+#pragma unroll
+  for (int k = 0; k < NSEQ; ++k) {
+    h[k][0] = h[k][1] = zero2();
+    b[k].zero();
+    c[k].zero();
+    if (k < ns) {
+      load_pairs<2>(state + (n0 + k) * ds + so, h[k]);
+      b[k].load(static_cast<const Tin*>(a.Bm) + (n0 + k) * a.B_stride + g * S + nl * 4);
+      c[k].load(static_cast<const Tin*>(a.Cm) + (n0 + k) * a.C_stride + g * S + nl * 4);
+    }
+  }
+  // this lane's own sequence (all lanes the only one with NSEQ = 1)
+  const int own = NSEQ == 1 ? 0 : nl;
+  const bool mine = own < ns;
+  float x = 0.f, z = 0.f, dt[1] = {0.f};
+  if (mine) {
+    const int64_t n = n0 + own;
     x = Elem<Tin>::load(static_cast<const Tin*>(a.x) + n * a.x_stride + d);
-    float dt = Elem<Tin>::load(static_cast<const Tin*>(a.delta) + n * a.delta_stride + d);
-    if (a.delta_bias) dt += a.delta_bias[d];
-    dt = step_size(dt, a.softplus);
-    const float u = dt * x;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      h[i] = fmaf(ex2(dt * (A[i] * kLog2e)), h[i], u * b[i]);
-      y = fmaf(c[i], h[i], y);
-    }
-    store_vec<4>(st, h);
+    dt[0] = Elem<Tin>::load(static_cast<const Tin*>(a.delta) + n * a.delta_stride + d);
+    if (a.z) z = Elem<Tin>::load(static_cast<const Tin*>(a.z) + n * a.z_stride + d);
+    if (a.delta_bias) dt[0] += a.delta_bias[d];
   }
+  if (ns > 0) load_vec<float, 4>(a.A + so, A2);
+  step_sizes<1>(dt, a.softplus);
+  const float u = dt[0] * x;
+  float y[4] = {};
 #pragma unroll
-  for (int o = LN / 2; o > 0; o >>= 1) y += __shfl_xor_sync(0xffffffffu, y, o);
-  if (live && nl == 0) {
-    if (a.D_skip) y = fmaf(a.D_skip[d], x, y);
-    if (a.z) {
-      const float zz = Elem<Tin>::load(static_cast<const Tin*>(a.z) + n * a.z_stride + d);
-      y *= zz * sigmoid_fast(zz);
-    }
-    Elem<Tin>::store(static_cast<Tin*>(a.out) + n * a.D + d, y);
+  for (int k = 0; k < NSEQ; ++k) {
+    const float sk = NSEQ == 1 ? dt[0] : __shfl_sync(0xffffffffu, dt[0], k, LN);
+    const float uk = NSEQ == 1 ? u : __shfl_sync(0xffffffffu, u, k, LN);
+    const float sl = sk * kLog2e;
+    const f2 uu = pack2(uk, uk);
+    const f2 w0 = pack2(ex2(sl * A2[0]), ex2(sl * A2[1]));
+    const f2 w1 = pack2(ex2(sl * A2[2]), ex2(sl * A2[3]));
+    h[k][0] = fma2(w0, h[k][0], mul2(uu, pack2(b[k].at(0), b[k].at(1))));
+    h[k][1] = fma2(w1, h[k][1], mul2(uu, pack2(b[k].at(2), b[k].at(3))));
+    if (k < ns) store_pairs<2>(state + (n0 + k) * ds + so, h[k]);
+    y[k] = sum2(fma2(pack2(c[k].at(2), c[k].at(3)), h[k][1],
+                     mul2(pack2(c[k].at(0), c[k].at(1)), h[k][0])));
   }
+  float out;
+  if constexpr (NSEQ == 1) {
+    out = y[0];
+#pragma unroll
+    for (int o = LN / 2; o > 0; o >>= 1) out += __shfl_xor_sync(0xffffffffu, out, o);
+  } else {
+    out = sum_lanes<LN>(y, nl).x;
+  }
+  if (mine && nl < NSEQ) {
+    if (a.D_skip) out = fmaf(a.D_skip[d], x, out);
+    if (a.z) out *= z * sigmoid2(z);
+    Elem<Tin>::store(static_cast<Tin*>(a.out) + (n0 + own) * a.D + d, out);
+  }
+}
+
+// Packed batches: validates the offsets, then chooses the segment length (a.seg
+// .seg_len where a sequence is longer than that, else the whole batch's
+// length, so that every sequence is one unit) and writes seg_off and order.
+constexpr int kMaxOrder = 2048;
+
+__global__ void __launch_bounds__(1024) scan_plan_kernel(const int32_t* __restrict__ cu, int N,
+                                                         int T, StatusBlock* sb, int seg_len,
+                                                         int32_t* __restrict__ seg_off,
+                                                         int32_t* __restrict__ order) {
+  __shared__ int bad, longest, carry;
+  __shared__ int wsum[32], lens[kMaxOrder];
+  const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
+  if (tid == 0) {
+    bad = (cu[0] != 0 || cu[N] != T) ? 1 : 0;
+    longest = 0;
+    carry = 0;
+  }
+  __syncthreads();
+  int most = 0;
+  for (int n = tid; n < N; n += 1024) {
+    const int len = cu[n + 1] - cu[n];
+    if (cu[n + 1] < cu[n]) atomicOr(&bad, 1);
+    most = max(most, len);
+    if (n < kMaxOrder) lens[n] = len;
+  }
+  atomicMax(&longest, most);
+  __syncthreads();
+  if (tid == 0) {
+    sb->status = bad ? KDA_ERR_BAD_SEQLENS : KDA_OK;
+    sb->detail = 0;
+    sb->never_set = 0;
+    sb->seqlens_ok = bad ? 0 : 1;
+    sb->pad[0] = longest > seg_len ? seg_len : T;
+  }
+  if (bad) return;
+  const int sl = longest > seg_len ? seg_len : T;
+  // longest first; batches of more sequences keep their order
+  for (int n = tid; n < N; n += 1024) {
+    int rank = n;
+    if (N <= kMaxOrder) {
+      const int len = lens[n];
+      rank = 0;
+      for (int m = 0; m < N; ++m) rank += lens[m] > len || (lens[m] == len && m < n);
+    }
+    order[rank] = n;
+  }
+  // exclusive prefix sums of the segment counts, 1024 sequences a step
+  for (int n0 = 0; n0 < N; n0 += 1024) {
+    const int n = n0 + tid;
+    int c = 0;
+    if (n < N) {
+      const int len = cu[n + 1] - cu[n];
+      c = len > 0 ? 1 + (len - 1) / sl : 1;
+    }
+    int s = c;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int v = __shfl_up_sync(0xffffffffu, s, o);
+      if (lane >= o) s += v;
+    }
+    if (lane == 31) wsum[wid] = s;
+    __syncthreads();
+    if (wid == 0) {
+      int v = wsum[lane];
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int u = __shfl_up_sync(0xffffffffu, v, o);
+        if (lane >= o) v += u;
+      }
+      wsum[lane] = v;
+    }
+    __syncthreads();
+    const int before = carry + (wid ? wsum[wid - 1] : 0) + s - c;
+    if (n < N) seg_off[n] = before;
+    if (n == N - 1) seg_off[N] = before + c;
+    __syncthreads();
+    if (tid == 0) carry += wsum[31];
+    __syncthreads();
+  }
+}
+
+template <typename Tin, int S, int SC, int MODE>
+cudaError_t launch_one(const Args& a, cudaStream_t st) {
+  using L = Layout<S, SC>;
+  constexpr size_t bytes = Smem<Tin, S, SC, MODE>::bytes();
+  if (bytes > 48 * 1024)
+    if (cudaError_t e = cudaFuncSetAttribute(scan_fwd_kernel<Tin, S, SC, MODE>,
+                                             cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                             (int)bytes))
+      return e;
+  const unsigned grid = (unsigned)((int64_t)a.seg.units * channel_blocks(a.D, a.G, L::CT));
+  scan_fwd_kernel<Tin, S, SC, MODE><<<grid, L::NT, bytes, st>>>(a);
+  return cudaGetLastError();
 }
 
 template <typename Tin, int MODE>
 cudaError_t launch_mode(const Args& a, cudaStream_t st) {
-  const unsigned grid = (unsigned)((int64_t)a.seg.units * a.nblk);
-  switch (a.S) {
-    case 8: scan_fwd_kernel<Tin, 8, MODE><<<grid, Layout<8>::NT, 0, st>>>(a); break;
-    case 16: scan_fwd_kernel<Tin, 16, MODE><<<grid, Layout<16>::NT, 0, st>>>(a); break;
-    case 32: scan_fwd_kernel<Tin, 32, MODE><<<grid, Layout<32>::NT, 0, st>>>(a); break;
-    case 64: scan_fwd_kernel<Tin, 64, MODE><<<grid, Layout<64>::NT, 0, st>>>(a); break;
-    default: scan_fwd_kernel<Tin, 128, MODE><<<grid, Layout<128>::NT, 0, st>>>(a); break;
+  if (a.seg.wide) {
+    switch (a.S) {
+      case 8: return launch_one<Tin, 8, 1, MODE>(a, st);  // the lanes of a channel pair are few
+      case 16: return launch_one<Tin, 16, 2, MODE>(a, st);
+      case 32: return launch_one<Tin, 32, 2, MODE>(a, st);
+      case 64: return launch_one<Tin, 64, 2, MODE>(a, st);
+      default: return launch_one<Tin, 128, 2, MODE>(a, st);
+    }
   }
-  return cudaGetLastError();
+  switch (a.S) {
+    case 8: return launch_one<Tin, 8, 1, MODE>(a, st);
+    case 16: return launch_one<Tin, 16, 1, MODE>(a, st);
+    case 32: return launch_one<Tin, 32, 1, MODE>(a, st);
+    case 64: return launch_one<Tin, 64, 1, MODE>(a, st);
+    default: return launch_one<Tin, 128, 1, MODE>(a, st);
+  }
 }
 
 template <int MODE>
@@ -325,25 +615,44 @@ cudaError_t launch_typed(const Args& a, kda_dtype dt, cudaStream_t st) {
                         : launch_mode<float, MODE>(a, st);
 }
 
+template <typename Tin, int S>
+cudaError_t launch_step_s(const Args& a, float* state, int N, cudaStream_t st) {
+  if constexpr (S >= 16) {
+    constexpr int NSEQ = 4;
+    const int64_t many = ((int64_t)N + NSEQ - 1) / NSEQ * a.D * (S / 4);
+    if (many >= 148 * 1024) {  // every SM has 1024 threads with four sequences each
+      scan_step_kernel<Tin, S, NSEQ><<<(unsigned)((many + 255) / 256), 256, 0, st>>>(a, state, N);
+      return cudaGetLastError();
+    }
+  }
+  const int64_t all = (int64_t)N * a.D * (S / 4);
+  scan_step_kernel<Tin, S, 1><<<(unsigned)((all + 255) / 256), 256, 0, st>>>(a, state, N);
+  return cudaGetLastError();
+}
+
 template <typename Tin>
 cudaError_t launch_step(const Args& a, float* state, int N, cudaStream_t st) {
-  const int64_t items = (int64_t)N * a.D * a.S / 4;
-  const unsigned grid = (unsigned)((items + 255) / 256);
   switch (a.S) {
-    case 8: scan_step_kernel<Tin, 8><<<grid, 256, 0, st>>>(a, state, N); break;
-    case 16: scan_step_kernel<Tin, 16><<<grid, 256, 0, st>>>(a, state, N); break;
-    case 32: scan_step_kernel<Tin, 32><<<grid, 256, 0, st>>>(a, state, N); break;
-    case 64: scan_step_kernel<Tin, 64><<<grid, 256, 0, st>>>(a, state, N); break;
-    default: scan_step_kernel<Tin, 128><<<grid, 256, 0, st>>>(a, state, N); break;
+    case 8: return launch_step_s<Tin, 8>(a, state, N, st);
+    case 16: return launch_step_s<Tin, 16>(a, state, N, st);
+    case 32: return launch_step_s<Tin, 32>(a, state, N, st);
+    case 64: return launch_step_s<Tin, 64>(a, state, N, st);
+    default: return launch_step_s<Tin, 128>(a, state, N, st);
   }
-  return cudaGetLastError();
 }
 
 }  // namespace
 
+cudaError_t launch_scan_plan(const Args& a, int32_t* seg_off, int32_t* order, cudaStream_t st) {
+  scan_plan_kernel<<<1, 1024, 0, st>>>(a.seg.cu, a.seg.num_seqs, a.seg.T, a.sb, a.seg.seg_len,
+                                       seg_off, order);
+  return cudaGetLastError();
+}
+
 cudaError_t launch_ends(const Args& a, kda_dtype dt, cudaStream_t st) {
   if (cudaError_t e = a.g_seg ? launch_typed<kEnds>(a, dt, st) : launch_typed<kEnd>(a, dt, st))
     return e;
+  if (!a.split) return cudaSuccess;
   const int64_t items = (int64_t)a.seg.num_seqs * a.D * a.S / 4;
   scan_combine_kernel<<<(unsigned)((items + 255) / 256), 256, 0, st>>>(a);
   return cudaGetLastError();
@@ -351,35 +660,46 @@ cudaError_t launch_ends(const Args& a, kda_dtype dt, cudaStream_t st) {
 
 bool sizes_ok(int D, int S, int G) {
   if (S != 8 && S != 16 && S != 32 && S != 64 && S != 128) return false;
-  if (D % 8 != 0 || D > (1 << 24) || D % G != 0) return false;
-  return G == 1 || D / G % 32 == 0;
+  return D <= (1 << 24) && D % G == 0 && D / G % 8 == 0;
 }
 
-// Tokens per segment.  A segment costs a second pass over its tokens, so a
-// sequence is cut only where the channel blocks of the sequences do not fill
-// the GPU.
-int segment_len(int B, int T, int D, int S, bool packed) {
-  const int64_t blocks = (D + chan_tile(S) - 1) / chan_tile(S);
-  const int64_t slots = 148 * 4;
-  int64_t len;
-  if (packed) {
-    len = (int64_t)T * blocks / (slots * 2);
-  } else {
-    if (B * blocks >= slots / 2) return T;
-    const int64_t cuts = (slots + B * blocks - 1) / (B * blocks);
-    len = (T + cuts - 1) / cuts;
-  }
-  if (len < 256) len = 256;
-  len = (len + 31) / 32 * 32;
-  return (int)(len < T ? len : T);
-}
-
-Segments plan_segments(const int32_t* cu, int num_seqs, int B, int T, int D, int S) {
+// How a batch is spread over the GPU.  `warps` is its sequences' warps with two
+// channels a thread; 592 schedulers want two to four each.  Dense batches:
+//   from 8 a scheduler's four warps on (SMs x 8): two channels a thread;
+//   from SMs x 3: one channel a thread, twice the warps;
+//   fewer: the sequences are cut until there are SMs x 16 warps, which costs
+//   a second pass over all but the last segments.
+// Packed batches do not show their lengths to the host: one channel a thread
+// unless there are many sequences, and a cut (the plan kernel's choice) only
+// where a sequence is longer than the time that the whole batch takes.  The
+// gradients' walk has two warps a scheduler at most (its registers) and wants
+// both; its first pass over the segments is needed anyway.
+Segments plan_segments(const int32_t* cu, int num_seqs, int B, int T, int D, int S, bool bwd) {
+  constexpr int64_t kSms = 148;
   Segments m{};
   m.cu = cu;
   m.num_seqs = cu ? num_seqs : B;
   m.T = T;
-  m.seg_len = segment_len(B, T, D, S, cu != nullptr);
+  const int64_t per_seq = ((int64_t)D * S + 255) / 256;
+  const int64_t warps = m.num_seqs * per_seq;
+  int64_t len = T;
+  if (cu) {
+    m.wide = true;
+    len = 3 * T * per_seq / (kSms * 16);
+    if (len < 256) len = 256;
+  } else {
+    m.wide = warps >= kSms * 8;
+    if (warps < kSms * (bwd ? 12 : 3)) {
+      int64_t segs = kSms * (bwd ? 12 : 16) / warps;
+      if (segs > T / 64) segs = T / 64;
+      if (segs >= 2) {
+        m.wide = true;
+        len = (T + segs - 1) / segs;
+      }
+    }
+  }
+  len = (len + kTile - 1) / kTile * kTile;
+  m.seg_len = (int)(len < T ? len : T);
   m.segs = (T + m.seg_len - 1) / m.seg_len;
   m.units = cu ? num_seqs + T / m.seg_len : B * m.segs;
   return m;
@@ -420,7 +740,6 @@ Args scan_args(const void* x, int64_t x_stride, const void* delta, int64_t delta
   a.D = D;
   a.S = S;
   a.G = G;
-  a.nblk = (D + chan_tile(S) - 1) / chan_tile(S);
   return a;
 }
 
@@ -437,9 +756,9 @@ size_t kda_selective_scan_fwd_workspace_size(int B, int T, int D, int S, int G, 
       (int64_t)B * T > kMaxRows)
     return 0;
   static const int32_t packed = 0;  // only whether there are offsets matters here
-  const Segments m = plan_segments(num_seqs > 0 && B == 1 ? &packed : nullptr, num_seqs, B, T, D, S);
+  const Segments m = plan_segments(num_seqs > 0 && B == 1 ? &packed : nullptr, num_seqs, B, T, D, S, false);
   size_t b = kStatusBytes;
-  if (m.cu) b += align256(sizeof(int32_t) * ((size_t)num_seqs + 1));
+  if (m.cu) b += 2 * align256(sizeof(int32_t) * ((size_t)num_seqs + 1));
   if (m.segs > 1)
     b += align256(sizeof(float) * (size_t)m.units * D * S) +
          align256(sizeof(float) * (size_t)m.units * D);
@@ -488,8 +807,9 @@ kda_status kda_selective_scan_fwd(const void* x, int64_t x_stride, const void* d
   if (workspace_bytes < need) return KDA_ERR_WORKSPACE;
   Args a = scan_args(x, x_stride, delta, delta_stride, A, Bm, B_stride, Cm, C_stride, D_skip, z,
                      z_stride, delta_bias, delta_softplus, D, S, G);
-  a.seg = plan_segments(cu_seqlens, num_seqs, B, T, D, S);
-  if ((int64_t)a.seg.units * a.nblk > 0x7fffffffLL || N * D / 256 * (S / 4) > 0x7ffffff0LL)
+  a.seg = plan_segments(cu_seqlens, num_seqs, B, T, D, S, false);
+  if ((int64_t)a.seg.units * channel_blocks(D, G, 8) > 0x7fffffffLL ||
+      N * D / 256 * (S / 4) > 0x7ffffff0LL)
     return KDA_ERR_UNSUPPORTED;
   a.init = init_state;
   a.final_state = final_state;
@@ -498,18 +818,21 @@ kda_status kda_selective_scan_fwd(const void* x, int64_t x_stride, const void* d
   char* tail = static_cast<char*>(workspace) + kStatusBytes;
   cudaStream_t st = (cudaStream_t)stream;
   if (cu_seqlens) {
+    const size_t part = align256(sizeof(int32_t) * ((size_t)num_seqs + 1));
     int32_t* off = reinterpret_cast<int32_t*>(tail);
-    tail += align256(sizeof(int32_t) * ((size_t)num_seqs + 1));
+    int32_t* order = reinterpret_cast<int32_t*>(tail + part);
+    tail += 2 * part;
     a.seg.seg_off = off;
-    if (cudaError_t e = launch_seqlens_plan(cu_seqlens, num_seqs, T, a.sb, a.seg.seg_len, off, st))
-      return cuda_failure(e);
+    a.seg.order = order;
+    if (cudaError_t e = launch_scan_plan(a, off, order, st)) return cuda_failure(e);
   }
-  if (a.seg.segs > 1) {
+  a.split = a.seg.segs > 1;
+  if (a.split) {
     a.h_seg = reinterpret_cast<float*>(tail);
     tail += align256(sizeof(float) * (size_t)a.seg.units * D * S);
     a.dt_sum = reinterpret_cast<float*>(tail);
   }
-  if (a.h_seg)
+  if (a.split)
     if (cudaError_t e = launch_ends(a, in_dtype, st)) return cuda_failure(e);
   const cudaError_t e = launch_typed<kOut>(a, in_dtype, st);
   return e == cudaSuccess ? KDA_OK : cuda_failure(e);

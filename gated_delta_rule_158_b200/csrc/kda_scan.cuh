@@ -1,5 +1,5 @@
-// kda_scan.cuh -- shared by the selective scan's forward and gradients: thread
-// layout, segments of long sequences, arguments.
+// kda_scan.cuh -- shared by the selective scan's forward and gradients: units
+// of work, arguments, packed fp32 arithmetic.
 #pragma once
 
 #include "kda_layer.cuh"
@@ -9,57 +9,55 @@ namespace scan {
 
 constexpr float kLog2e = 1.4426950408889634f;
 
-// A channel's S states lie in LN lanes, 4 a lane, so that a warp holds 32 / LN
-// channels and every thread has four independent recurrences; a CTA of NT
-// threads holds CT channels (32, or 16 at S = 128 where 32 would be 1024
-// threads).
-template <int S>
-struct Layout {
-  static constexpr int LN = S / 4;
-  static constexpr int NT = LN * 32 > 512 ? 512 : LN * 32;
-  static constexpr int CT = NT / LN;
-};
-
-inline int chan_tile(int S) { return S == 128 ? 16 : 32; }
-
 // The tokens are one flat axis; a unit is one segment (at most seg_len tokens)
-// of one sequence.  Dense: segs units per sequence.  Packed: seg_off[n] units
-// before sequence n.
+// of one sequence.  Dense: segs units per sequence.  Packed: the plan kernel
+// has chosen seg_len (in the status block) and written seg_off[n], the units
+// before sequence n, and order, the sequences longest first; with one unit per
+// sequence, unit u is sequence order[u].
 struct Segments {
   const int32_t* cu;       // nullptr = dense
   const int32_t* seg_off;  // packed
+  const int32_t* order;    // packed
   int num_seqs, T, seg_len, segs, units;
+  bool wide;               // forward: two channels a thread
 };
 
 struct Unit {
-  int n, k;          // sequence, segment of it
+  int n;             // sequence
+  int slot;          // index of the segment's states, in token order
   int64_t t0, t1;    // its tokens
   bool first, last;  // of its sequence
   bool valid;
 };
 
-__device__ __forceinline__ Unit resolve(const Segments& m, int unit) {
+__device__ __forceinline__ Unit resolve(const Segments& m, const StatusBlock* sb, int unit) {
   Unit u;
   int64_t start, end;
+  int k, len = m.seg_len;
   if (m.cu) {
-    u.valid = unit < __ldg(m.seg_off + m.num_seqs);
+    const int all = __ldg(m.seg_off + m.num_seqs);
+    u.valid = unit < all;
     if (!u.valid) return u;
-    u.n = find_range(m.seg_off, m.num_seqs, unit);
-    u.k = unit - __ldg(m.seg_off + u.n);
-    u.last = unit + 1 == __ldg(m.seg_off + u.n + 1);
+    len = sb->pad[0];
+    u.n = all == m.num_seqs ? __ldg(m.order + unit) : find_range(m.seg_off, m.num_seqs, unit);
+    const int before = __ldg(m.seg_off + u.n);
+    k = all == m.num_seqs ? 0 : unit - before;
+    u.slot = before + k;
+    u.last = u.slot + 1 == __ldg(m.seg_off + u.n + 1);
     start = __ldg(m.cu + u.n);
     end = __ldg(m.cu + u.n + 1);
   } else {
     u.valid = true;
     u.n = unit / m.segs;
-    u.k = unit - u.n * m.segs;
-    u.last = u.k == m.segs - 1;
+    k = unit - u.n * m.segs;
+    u.slot = unit;
+    u.last = k == m.segs - 1;
     start = (int64_t)u.n * m.T;
     end = start + m.T;
   }
-  u.first = u.k == 0;
-  u.t0 = start + (int64_t)u.k * m.seg_len;
-  u.t1 = u.last ? end : u.t0 + m.seg_len;
+  u.first = k == 0;
+  u.t0 = start + (int64_t)k * len;
+  u.t1 = u.last ? end : u.t0 + len;
   return u;
 }
 
@@ -77,8 +75,9 @@ struct Args {
   const float* init;
   float* final_state;
   void* out;
-  int D, S, G, nblk;
+  int D, S, G;
   Segments seg;
+  bool split;     // some sequence may have more than one segment
   float* h_seg;   // [units][D][S]: a segment's end state from zero, then its incoming state
   float* dt_sum;  // [units][D]: the segment's sum of dt
   StatusBlock* sb;
@@ -90,22 +89,194 @@ struct Args {
   float* dz;
   float* d_init;
   float* g_seg;    // [units][D][S]: as h_seg, of the state gradient, from the right
-  float* ckpt;     // [tokens / step][D][S]: states in front of every step-th token
-  float* dbc_part; // [nblk][tokens][2][S]: dBm, dCm summed over a channel block
+  float* ckpt;     // [tiles][D][S]: the segment's own states in front of every kStep tokens
+  float* ckpt_dt;  // [tiles][D]: its sum of dt up to there
+  float* dbc_part; // [channel blocks][tokens][2][S]: dBm, dCm summed over a channel block
   float* da_part;  // [units][D][S]
   float* dd_part;  // [units][2][D]: dD_skip, ddelta_bias
 };
 
+constexpr int kStep = 8;  // tokens between the states kept for the gradients
+
+// first checkpoint slot of a unit: units lie in token order by slot, so the
+// ranges do not meet
+__device__ __forceinline__ int64_t first_tile(const Unit& u) { return u.t0 / kStep + u.slot; }
+
+// A block's channels: block cb of the per_group blocks of each group
+struct Channels {
+  int g, d0, n;
+};
+template <int CT>
+__device__ __forceinline__ Channels channels_of(const Args& a, int cb) {
+  const int Dg = a.D / a.G, per = (Dg + CT - 1) / CT;
+  Channels c;
+  c.g = cb / per;
+  const int k = cb - c.g * per;
+  c.d0 = c.g * Dg + k * CT;
+  c.n = min(CT, Dg - k * CT);
+  return c;
+}
+inline int channel_blocks(int D, int G, int CT) { return G * ((D / G + CT - 1) / CT); }
+
+// ------------------------------------------------------------- arithmetic
 __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
 
-// dt from the raw step: log(1 + e^v) = max(v, 0) + log1p(e^-|v|)
-__device__ __forceinline__ float step_size(float v, bool softplus) {
-  return softplus ? fmaxf(v, 0.f) + log1pf(__expf(-fabsf(v))) : v;
+// two fp32 values side by side, one instruction for both
+using f2 = unsigned long long;
+__device__ __forceinline__ f2 pack2(float a, float b) {
+  f2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
 }
+__device__ __forceinline__ void unpack2(f2 v, float& a, float& b) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
+}
+__device__ __forceinline__ f2 fma2(f2 a, f2 b, f2 c) {
+  f2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ f2 mul2(f2 a, f2 b) {
+  f2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ f2 add2(f2 a, f2 b) {
+  f2 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ f2 ex2_2(f2 v) {
+  float a, b;
+  unpack2(v, a, b);
+  return pack2(ex2(a), ex2(b));
+}
+__device__ __forceinline__ float sum2(f2 v) {
+  float a, b;
+  unpack2(v, a, b);
+  return a + b;
+}
+__device__ __forceinline__ f2 zero2() { return 0ull; }
+
+// 2 N consecutive floats as N pairs (aligned to their size)
+template <int N>
+__device__ __forceinline__ void load_pairs(const float* p, f2 (&v)[N]) {
+  if constexpr (N == 1) {
+    v[0] = *reinterpret_cast<const f2*>(p);
+  } else {
+    const ulonglong2 u = *reinterpret_cast<const ulonglong2*>(p);
+    v[0] = u.x;
+    v[1] = u.y;
+  }
+}
+template <int N>
+__device__ __forceinline__ void store_pairs(float* p, const f2 (&v)[N]) {
+  if constexpr (N == 1) *reinterpret_cast<f2*>(p) = v[0];
+  else *reinterpret_cast<ulonglong2*>(p) = make_ulonglong2(v[0], v[1]);
+}
+
+// log(1 + u) for 0 <= u <= 1 as u P(u): P is the polynomial of degree 8 nearest
+// to log(1 + u) / u in relative error (weighted least squares on 4000 Chebyshev
+// points, the weights raised where the error is largest until it is level:
+// 3.0e-8; 1.7e-7 with the fp32 rounding of the evaluation).  Small u keep their
+// relative accuracy, which log2 of the rounded sum 1 + u would lose.
+__device__ __forceinline__ f2 log1p_unit(f2 u) {
+  f2 p = pack2(0.005232690833508968f, 0.005232690833508968f);
+  p = fma2(p, u, pack2(-0.029505228623747826f, -0.029505228623747826f));
+  p = fma2(p, u, pack2(0.07822594791650772f, 0.07822594791650772f));
+  p = fma2(p, u, pack2(-0.13663245737552643f, -0.13663245737552643f));
+  p = fma2(p, u, pack2(0.19106008112430573f, 0.19106008112430573f));
+  p = fma2(p, u, pack2(-0.2484298199415207f, -0.2484298199415207f));
+  p = fma2(p, u, pack2(0.3331909775733948f, 0.3331909775733948f));
+  p = fma2(p, u, pack2(-0.4999949336051941f, -0.4999949336051941f));
+  p = fma2(p, u, pack2(0.9999999403953552f, 0.9999999403953552f));
+  return mul2(p, u);
+}
+
+// dt from the raw steps: log(1 + e^v) = max(v, 0) + log1p(e^-|v|), two at a time
+template <int V>
+__device__ __forceinline__ void step_sizes(float (&v)[V], bool softplus) {
+  if (!softplus) return;
+#pragma unroll
+  for (int j = 0; j < V; j += 2) {
+    const float b = V > 1 ? v[V > 1 ? j + 1 : 0] : 0.f;
+    float p, q;
+    unpack2(log1p_unit(pack2(ex2(-kLog2e * fabsf(v[j])), ex2(-kLog2e * fabsf(b)))), p, q);
+    v[j] = fmaxf(v[j], 0.f) + p;
+    if (V > 1) v[V > 1 ? j + 1 : 0] = fmaxf(b, 0.f) + q;
+  }
+}
+
+__device__ __forceinline__ float sigmoid2(float x) {
+  return __fdividef(1.0f, 1.0f + ex2(-kLog2e * x));
+}
+
+// ------------------------------------------------------- asynchronous copies
+// BYTES (4, 8, 16 or 32) from global to shared memory without registers; zeros
+// where !in (the source is not read then)
+template <int BYTES>
+__device__ __forceinline__ void copy_in(char* to, const void* from, bool in) {
+  constexpr int N = BYTES < 16 ? BYTES : 16;
+#pragma unroll
+  for (int i = 0; i < BYTES; i += N) {
+    const uint32_t dst = (uint32_t)__cvta_generic_to_shared(to + i);
+    const char* src = static_cast<const char*>(from) + i;
+    if constexpr (N == 16)
+      asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
+                   "r"(in ? 16 : 0)
+                   : "memory");
+    else
+      asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(dst), "l"(src), "n"(N),
+                   "r"(in ? N : 0)
+                   : "memory");
+  }
+}
+__device__ __forceinline__ void copies_issued() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+__device__ __forceinline__ void copies_landed() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+
+// V elements of a slot as fp32
+template <typename T, int V>
+__device__ __forceinline__ void read_slot(const char* p, float (&v)[V]) {
+  load_vec<T, V>(reinterpret_cast<const T*>(p), v);
+}
+
+// -------------------------------------------------------------- raw values
+// V elements as they lie in memory, so that loads stay in flight until their
+// first use
+template <typename T, int V>
+struct Raw {
+  static constexpr int BYTES = V * (int)sizeof(T);
+  static constexpr int N = BYTES < 4 ? 1 : BYTES / 4;
+  uint32_t r[N];
+  __device__ __forceinline__ void zero() {
+#pragma unroll
+    for (int i = 0; i < N; ++i) r[i] = 0;
+  }
+  __device__ __forceinline__ void load(const T* p) {
+    if constexpr (BYTES == 2) {
+      r[0] = *reinterpret_cast<const unsigned short*>(p);
+    } else if constexpr (BYTES == 4) {
+      r[0] = *reinterpret_cast<const uint32_t*>(p);
+    } else if constexpr (BYTES == 8) {
+      const uint2 u = *reinterpret_cast<const uint2*>(p);
+      r[0] = u.x; r[1] = u.y;
+    } else {
+#pragma unroll
+      for (int i = 0; i < N; i += 4) {
+        const uint4 u = reinterpret_cast<const uint4*>(p)[i / 4];
+        r[i] = u.x; r[i + 1] = u.y; r[i + 2] = u.z; r[i + 3] = u.w;
+      }
+    }
+  }
+  __device__ __forceinline__ float at(int i) const {
+    if constexpr (sizeof(T) == 4) return __uint_as_float(r[i]);
+    else return __uint_as_float(i & 1 ? r[i >> 1] & 0xffff0000u : r[i >> 1] << 16);
+  }
+};
 
 // Sums of four tokens' values over the LN lanes of a channel.  LN >= 4: lane
 // l & 3 returns token l & 3; LN = 2: lane l returns tokens 2 l and 2 l + 1.
@@ -128,13 +299,79 @@ __device__ __forceinline__ float2 sum_lanes(const float (&v)[4], int l) {
   }
 }
 
-// Tokens per segment, the units of a batch, workspace rounding (kda_scan.cu).
-Segments plan_segments(const int32_t* cu, int num_seqs, int B, int T, int D, int S);
+// Writes the sums of four tokens of SC neighbouring channels, P floats between
+// tokens.
+template <int SC, int LN, int P>
+__device__ __forceinline__ void store_sums(float* p, const float (&v)[SC][4], int l) {
+  float2 r[SC];
+#pragma unroll
+  for (int q = 0; q < SC; ++q) r[q] = sum_lanes<LN>(v[q], l);
+  if constexpr (LN == 2) {
+    float* at = p + 2 * l * P;
+    if constexpr (SC == 2) {
+      *reinterpret_cast<float2*>(at) = make_float2(r[0].x, r[1].x);
+      *reinterpret_cast<float2*>(at + P) = make_float2(r[0].y, r[1].y);
+    } else {
+      at[0] = r[0].x;
+      at[P] = r[0].y;
+    }
+  } else if (l < 4) {
+    if constexpr (SC == 2) *reinterpret_cast<float2*>(p + l * P) = make_float2(r[0].x, r[1].x);
+    else p[l * P] = r[0].x;
+  }
+}
+
+// dt and u of V channels of a token, as load_du reads them for SC neighbouring
+// channels: (dt, dt', u, u') per pair, or (dt, u) per channel
+template <int SC, int V>
+__device__ __forceinline__ void store_du(float* p, const float (&dt)[V], const float (&u)[V]) {
+  if constexpr (SC == 2) {
+#pragma unroll
+    for (int j = 0; j < V; j += 2)
+      *reinterpret_cast<float4*>(p + 2 * j) = make_float4(dt[j], dt[j + 1], u[j], u[j + 1]);
+  } else {
+#pragma unroll
+    for (int j = 0; j < V; ++j) *reinterpret_cast<float2*>(p + 2 * j) = make_float2(dt[j], u[j]);
+  }
+}
+// the first half of V channels' entries: what store_sums has put over dt
+template <int SC, int V>
+__device__ __forceinline__ void load_sums(const float* p, float (&v)[V]) {
+#pragma unroll
+  for (int j = 0; j < V; j += SC) {
+    if constexpr (SC == 2) {
+      const float2 f = *reinterpret_cast<const float2*>(p + 2 * j);
+      v[j] = f.x;
+      v[j + 1] = f.y;
+    } else {
+      v[j] = p[2 * j];
+    }
+  }
+}
+template <int SC>
+__device__ __forceinline__ void load_du(const float* p, float (&dt)[SC], float (&u)[SC]) {
+  if constexpr (SC == 2) {
+    const float4 v = *reinterpret_cast<const float4*>(p);
+    dt[0] = v.x; dt[1] = v.y; u[0] = v.z; u[1] = v.w;
+  } else {
+    const float2 v = *reinterpret_cast<const float2*>(p);
+    dt[0] = v.x; u[0] = v.y;
+  }
+}
+
+// ------------------------------------------------------------------- host
+// Tokens per segment, the units of a batch (kda_scan.cu).
+Segments plan_segments(const int32_t* cu, int num_seqs, int B, int T, int D, int S, bool bwd);
 bool sizes_ok(int D, int S, int G);
 inline size_t align256(size_t b) { return (b + 255) / 256 * 256; }
 
-// The segments' local end states (and, with g_seg, state gradients at their
-// starts) and their combination into h_seg, g_seg.
+// Packed batches: validates the offsets, chooses seg_len and writes seg_off and
+// order (both [num_seqs + 1]).
+cudaError_t launch_scan_plan(const Args& a, int32_t* seg_off, int32_t* order, cudaStream_t st);
+
+// Each segment's own end state (h_seg) and sum of dt, with g_seg the state
+// gradient its outputs send to its start, with ckpt its states on the way; then
+// with split their combination into incoming h_seg and g_seg.
 cudaError_t launch_ends(const Args& a, kda_dtype dt, cudaStream_t st);
 
 kda_status check_scan(kda_dtype dt, int D, int S, int G, int64_t xs, int64_t ds, int64_t bs,

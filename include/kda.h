@@ -470,8 +470,8 @@ KDA_API kda_status kda_short_conv_bwd(const void *x, int64_t x_stride, const flo
  *                which run side by side; 0 for unsupported sizes)
  * States and sums are fp32; out is rounded once.  A zero-length sequence has
  * final = init.
- * Supported: S in {8, 16, 32, 64, 128}; D a multiple of 8; G dividing D, with
- * D / G a multiple of 32 where G > 1; B * T <= 2^31 - 2^16.
+ * Supported: S in {8, 16, 32, 64, 128}; G dividing D and D / G a multiple of
+ * 8; B * T <= 2^31 - 2^16.
  */
 KDA_API size_t kda_selective_scan_fwd_workspace_size(int B, int T, int D, int S, int G,
                                                      int num_seqs);

@@ -136,7 +136,7 @@ SHARED_SCAN = [
     (dict(x=None), INV), (dict(dl=None), INV), (dict(A=None), INV), (dict(Bm=None), INV),
     (dict(Cm=None), INV), (dict(dt=5), INV), (dict(D=0), INV), (dict(G=0), INV),
     (dict(S=24, bs=24, cs=24), UNS), (dict(S=256, bs=256, cs=256), UNS), (dict(S=4), UNS),
-    (dict(D=52), UNS), (dict(G=3, bs=48, cs=48), UNS), (dict(G=4, bs=64, cs=64), UNS),
+    (dict(D=52), UNS), (dict(G=3, bs=48, cs=48), UNS), (dict(G=16, bs=256, cs=256), UNS),
     (dict(xs=48), INV), (dict(dls=68), INV), (dict(bs=8), INV), (dict(cs=20), INV),
     (dict(zs=0), INV), (dict(z=at(6) + 2), MIS), (dict(A=at(2) + 4), MIS),
 ]
