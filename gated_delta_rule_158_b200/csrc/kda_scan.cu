@@ -54,7 +54,8 @@ struct Smem {
   using L = Layout<S, SC>;
   // fp32 rows of the tile, offsets in floats
   static constexpr int kDu = 0;  // [token] store_du; behind the scan the outputs y
-  static constexpr int kDy = kDu + 2 * kTile * L::CT;
+  static constexpr int kRow = kDuRow<SC, L::CT>;
+  static constexpr int kDy = kDu + kTile * kRow;
   static constexpr int kB = kDy + (MODE == kEnds ? kTile * L::CT : 0);
   static constexpr int kC = kB + kTile * S;
   static constexpr int kRows = kC + (MODE == kEnd ? 0 : kTile * S);
@@ -187,7 +188,7 @@ __global__ void __launch_bounds__(Layout<S, SC_>::NT) scan_fwd_kernel(const Args
         u[j] *= dt[j];
         if (MODE != kOut) dsum[j] += dt[j];
       }
-      store_du<SC, VEC>(sm + M::kDu + t * 2 * CT + 2 * ic, dt, u);
+      store_du<SC, VEC>(sm + M::kDu + t * M::kRow, ic, dt, u);
       if (MODE == kEnds) {
         float dy[VEC], z[VEC];
         read_slot<Tin, VEC>(slot(i, 3, m), dy);
@@ -223,14 +224,14 @@ __global__ void __launch_bounds__(Layout<S, SC_>::NT) scan_fwd_kernel(const Args
     f2 w[2][SC][2], b[2][2], c[2][2];
     float dt[2][SC], u[2][SC], dy[2][SC];
   };
-  float* pdu = sm + M::kDu + 2 * SC * cp;
+  float* pdu = sm + M::kDu + du_entry<SC>(SC * cp);
   const float* pdy = sm + M::kDy + SC * cp;
   const float* pb = sm + M::kB + nl * 4;
   const float* pc = sm + M::kC + nl * 4;
   auto fetch = [&](Pair& g, int t) {
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
-      load_du<SC>(pdu + (t + k) * 2 * CT, g.dt[k], g.u[k]);
+      load_du<SC>(pdu + (t + k) * M::kRow, g.dt[k], g.u[k]);
       load_pairs<2>(pb + (t + k) * S, g.b[k]);
       if (MODE != kEnd) load_pairs<2>(pc + (t + k) * S, g.c[k]);
       if (MODE == kEnds) load_vec<float, SC>(pdy + (t + k) * CT, g.dy[k]);
@@ -294,7 +295,7 @@ __global__ void __launch_bounds__(Layout<S, SC_>::NT) scan_fwd_kernel(const Args
         decays(g0);
         // y takes the place of the four tokens' dt: only the channel's lanes, all
         // of them in this warp, read it, and they have
-        if (MODE == kOut) store_sums<SC, LN, 2 * CT>(pdu + t4 * 2 * CT, y, nl);
+        if (MODE == kOut) store_sums<SC, LN, M::kRow>(pdu + t4 * M::kRow, y, nl);
       }
     }
   };
@@ -308,7 +309,7 @@ __global__ void __launch_bounds__(Layout<S, SC_>::NT) scan_fwd_kernel(const Args
         float y[VEC], x[VEC], z[VEC];
         read_slot<Tin, VEC>(slot(i, 0, m), x);
         if (a.z) read_slot<Tin, VEC>(slot(i, 2, m), z);
-        load_sums<SC, VEC>(sm + M::kDu + t * 2 * CT + 2 * ic, y);
+        load_sums<SC, VEC>(sm + M::kDu + t * M::kRow, ic, t, y);
 #pragma unroll
         for (int j = 0; j < VEC; ++j) {
           y[j] = fmaf(skip[j], x[j], y[j]);
@@ -689,8 +690,8 @@ Segments plan_segments(const int32_t* cu, int num_seqs, int B, int T, int D, int
     if (len < 256) len = 256;
   } else {
     m.wide = warps >= kSms * 8;
-    if (warps < kSms * (bwd ? 12 : 3)) {
-      int64_t segs = kSms * (bwd ? 12 : 16) / warps;
+    if (warps < kSms * (bwd ? 32 : 3)) {
+      int64_t segs = kSms * (bwd ? 32 : 16) / warps;
       if (segs > T / 64) segs = T / 64;
       if (segs >= 2) {
         m.wide = true;

@@ -299,63 +299,85 @@ __device__ __forceinline__ float2 sum_lanes(const float (&v)[4], int l) {
   }
 }
 
-// Writes the sums of four tokens of SC neighbouring channels, P floats between
-// tokens.
-template <int SC, int LN, int P>
-__device__ __forceinline__ void store_sums(float* p, const float (&v)[SC][4], int l) {
-  float2 r[SC];
-#pragma unroll
-  for (int q = 0; q < SC; ++q) r[q] = sum_lanes<LN>(v[q], l);
-  if constexpr (LN == 2) {
-    float* at = p + 2 * l * P;
-    if constexpr (SC == 2) {
-      *reinterpret_cast<float2*>(at) = make_float2(r[0].x, r[1].x);
-      *reinterpret_cast<float2*>(at + P) = make_float2(r[0].y, r[1].y);
-    } else {
-      at[0] = r[0].x;
-      at[P] = r[0].y;
-    }
-  } else if (l < 4) {
-    if constexpr (SC == 2) *reinterpret_cast<float2*>(p + l * P) = make_float2(r[0].x, r[1].x);
-    else p[l * P] = r[0].x;
-  }
+// The rows of dt and u: per token an entry of 4 floats (dt, dt', u, u') for two
+// neighbouring channels, or of 2 floats (dt, u) for one.  Rows of pairs are 16
+// floats longer than their entries, and every second eight entries change
+// places in pairs: so the fills (lanes two entries apart), the scan's reads
+// (lanes one entry apart) and the sums of four tokens, stored in the first
+// half of an entry for the first two and in the second half for the others,
+// meet no bank twice.
+template <int SC, int CT>
+constexpr int kDuRow = SC == 2 ? 2 * CT + 16 : 2 * CT;
+
+// entry of the channel (pair) that starts at channel c of the CTA
+template <int SC>
+__device__ __forceinline__ int du_entry(int c) {
+  if constexpr (SC == 1) return 2 * c;
+  const int cp = c >> 1;
+  return 4 * (cp ^ ((cp >> 3) & 1));
 }
 
-// dt and u of V channels of a token, as load_du reads them for SC neighbouring
-// channels: (dt, dt', u, u') per pair, or (dt, u) per channel
+// dt and u of V channels from c on
 template <int SC, int V>
-__device__ __forceinline__ void store_du(float* p, const float (&dt)[V], const float (&u)[V]) {
-  if constexpr (SC == 2) {
-#pragma unroll
-    for (int j = 0; j < V; j += 2)
-      *reinterpret_cast<float4*>(p + 2 * j) = make_float4(dt[j], dt[j + 1], u[j], u[j + 1]);
-  } else {
-#pragma unroll
-    for (int j = 0; j < V; ++j) *reinterpret_cast<float2*>(p + 2 * j) = make_float2(dt[j], u[j]);
-  }
-}
-// the first half of V channels' entries: what store_sums has put over dt
-template <int SC, int V>
-__device__ __forceinline__ void load_sums(const float* p, float (&v)[V]) {
+__device__ __forceinline__ void store_du(float* row, int c, const float (&dt)[V],
+                                         const float (&u)[V]) {
 #pragma unroll
   for (int j = 0; j < V; j += SC) {
-    if constexpr (SC == 2) {
-      const float2 f = *reinterpret_cast<const float2*>(p + 2 * j);
-      v[j] = f.x;
-      v[j + 1] = f.y;
-    } else {
-      v[j] = p[2 * j];
-    }
+    float* p = row + du_entry<SC>(c + j);
+    if constexpr (SC == 2)
+      *reinterpret_cast<float4*>(p) = make_float4(dt[j], dt[j + 1], u[j], u[j + 1]);
+    else
+      *reinterpret_cast<float2*>(p) = make_float2(dt[j], u[j]);
   }
 }
 template <int SC>
-__device__ __forceinline__ void load_du(const float* p, float (&dt)[SC], float (&u)[SC]) {
+__device__ __forceinline__ void load_du(const float* entry, float (&dt)[SC], float (&u)[SC]) {
   if constexpr (SC == 2) {
-    const float4 v = *reinterpret_cast<const float4*>(p);
+    const float4 v = *reinterpret_cast<const float4*>(entry);
     dt[0] = v.x; dt[1] = v.y; u[0] = v.z; u[1] = v.w;
   } else {
-    const float2 v = *reinterpret_cast<const float2*>(p);
+    const float2 v = *reinterpret_cast<const float2*>(entry);
     dt[0] = v.x; u[0] = v.y;
+  }
+}
+
+// The sums of tokens t4 .. t4 + 3 (t4 a multiple of 4) over a channel's lanes,
+// to the channels' entries of those tokens, P floats between tokens.
+template <int SC, int LN, int P>
+__device__ __forceinline__ void store_sums(float* entry, const float (&v)[SC][4], int l) {
+  float2 r[SC];
+#pragma unroll
+  for (int q = 0; q < SC; ++q) r[q] = sum_lanes<LN>(v[q], l);
+  if constexpr (SC == 2) {
+    if constexpr (LN == 2) {
+      float* at = entry + 2 * l * P + 2 * l;
+      *reinterpret_cast<float2*>(at) = make_float2(r[0].x, r[1].x);
+      *reinterpret_cast<float2*>(at + P) = make_float2(r[0].y, r[1].y);
+    } else if (l < 4) {
+      *reinterpret_cast<float2*>(entry + l * P + (l & 2)) = make_float2(r[0].x, r[1].x);
+    }
+  } else {
+    if constexpr (LN == 2) {
+      entry[2 * l * P] = r[0].x;
+      entry[2 * l * P + P] = r[0].y;
+    } else if (l < 4) {
+      entry[l * P] = r[0].x;
+    }
+  }
+}
+// what store_sums has put there, of V channels from c on of token t
+template <int SC, int V>
+__device__ __forceinline__ void load_sums(const float* row, int c, int t, float (&v)[V]) {
+#pragma unroll
+  for (int j = 0; j < V; j += SC) {
+    const float* p = row + du_entry<SC>(c + j);
+    if constexpr (SC == 2) {
+      const float2 f = *reinterpret_cast<const float2*>(p + (t & 2));
+      v[j] = f.x;
+      v[j + 1] = f.y;
+    } else {
+      v[j] = *p;
+    }
   }
 }
 

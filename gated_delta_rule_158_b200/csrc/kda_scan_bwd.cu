@@ -39,7 +39,7 @@ struct Walk {
   static constexpr int NT = S <= 32 ? 128 : 256;
   static constexpr int CT = 2 * NT / LN;           // channels of a CTA
   static constexpr int W = NT / 32;
-  static constexpr int kCtas = S <= 32 ? 3 : 1;    // per SM, by registers
+  static constexpr int kCtas = S <= 32 ? 2 : 1;    // per SM, by registers
   static constexpr int T = kWalk;
   static constexpr int PER = T * CT / NT;          // elements of a tile per thread
   static constexpr int VEC = PER > 4 ? 4 : PER < 2 ? 2 : PER;
@@ -48,7 +48,8 @@ struct Walk {
   static constexpr int BIT = T * S / NT < BPT ? 1 : T * S / NT / BPT;
   // fp32 rows of the tile, offsets in floats
   static constexpr int kDu = 0;                    // store_du; then the sums of dx, d(dt)
-  static constexpr int kDy = kDu + 2 * T * CT;     // [token][channel]; then y
+  static constexpr int kRow = kDuRow<2, CT>;
+  static constexpr int kDy = kDu + T * kRow;       // [token][channel]; then y
   static constexpr int kB = kDy + T * CT;
   static constexpr int kC = kB + T * S;
   static constexpr int kRed = kC + T * S;          // dB, dC [warp][T][2 S]
@@ -140,6 +141,13 @@ __device__ __forceinline__ f2 ex2_again(f2 v) {
   asm volatile("ex2.approx.ftz.f32 %0, %0;" : "+f"(a));
   asm volatile("ex2.approx.ftz.f32 %0, %0;" : "+f"(b));
   return pack2(a, b);
+}
+
+// an entry of the walk's sums: (gA, gA', gB, gB')
+__device__ __forceinline__ void load_pair_sums(const float* p, float* gA, float* gB) {
+  const float4 v = *reinterpret_cast<const float4*>(p);
+  gA[0] = v.x; gA[1] = v.y;
+  gB[0] = v.z; gB[1] = v.w;
 }
 
 template <typename Tin, int S>
@@ -257,7 +265,7 @@ __global__ void __launch_bounds__(Walk<S>::NT, Walk<S>::kCtas) scan_bwd_kernel(c
 #pragma unroll
           for (int j = 0; j < VEC; ++j) dy[j] *= z[j] * sigmoid2(z[j]);
         }
-        store_du<2, VEC>(sm + L::kDu + t * 2 * CT + 2 * ic, dt, u);
+        store_du<2, VEC>(sm + L::kDu + t * L::kRow, ic, dt, u);
         store_vec<VEC>(sm + L::kDy + t * CT + ic, dy);
         store_vec<VEC>(own_dt + m * NT * VEC, dt);
       }
@@ -293,7 +301,7 @@ __global__ void __launch_bounds__(Walk<S>::NT, Walk<S>::kCtas) scan_bwd_kernel(c
   };
   // tokens [s, s + kStep) of the tile
   auto walk = [&](int s, int step) {
-    float* pdu = sm + L::kDu + s * 2 * CT + 4 * cp;
+    float* pdu = sm + L::kDu + s * L::kRow + du_entry<2>(2 * cp);
     float* pdy = sm + L::kDy + s * CT + 2 * cp;
     const float* pb = sm + L::kB + s * S + nl * 4;
     const float* pc = sm + L::kC + s * S + nl * 4;
@@ -318,7 +326,7 @@ __global__ void __launch_bounds__(Walk<S>::NT, Walk<S>::kCtas) scan_bwd_kernel(c
       f2 b[2];
       float dt[2], u[2];
       load_pairs<2>(pb + t * S, b);
-      load_du<2>(pdu + t * 2 * CT, dt, u);
+      load_du<2>(pdu + t * L::kRow, dt, u);
 #pragma unroll
       for (int q = 0; q < 2; ++q) {
         const f2 dd = pack2(dt[q], dt[q]), uu = pack2(u[q], u[q]);
@@ -345,7 +353,7 @@ __global__ void __launch_bounds__(Walk<S>::NT, Walk<S>::kCtas) scan_bwd_kernel(c
         float dt[2], u[2], dys[2], gA[2], gB[2], yy[2];
         load_pairs<2>(pb + t * S, b);
         load_pairs<2>(pc + t * S, cc);
-        load_du<2>(pdu + t * 2 * CT, dt, u);
+        load_du<2>(pdu + t * L::kRow, dt, u);
         load_vec<float, 2>(pdy + t * CT, dys);
 #pragma unroll
         for (int q = 0; q < 2; ++q) {
@@ -386,7 +394,7 @@ __global__ void __launch_bounds__(Walk<S>::NT, Walk<S>::kCtas) scan_bwd_kernel(c
       // of them in this warp, and have read for the last time
 #pragma unroll
       for (int m = 0; m < 4; ++m) {
-        float* to = pdu + (t4 + m) * 2 * CT;
+        float* to = pdu + (t4 + m) * L::kRow;
         if constexpr (LN == 2) *reinterpret_cast<float2*>(to + 2 * nl) = gg[m];
         else if (nl < 4) to[nl] = gg[m].x;
         if (nl < 2) pdy[(t4 + m) * CT + nl] = y[m];
@@ -407,8 +415,9 @@ __global__ void __launch_bounds__(Walk<S>::NT, Walk<S>::kCtas) scan_bwd_kernel(c
       read_slot<Tin, VEC>(slot(i, 3, m), dy);
       if (a.z) read_slot<Tin, VEC>(slot(i, 2, m), z);
       load_vec<float, VEC>(own_dt + m * NT * VEC, dt);
-      load_sums<2, VEC>(sm + L::kDu + t * 2 * CT + 2 * ic, gA);
-      load_sums<2, VEC>(sm + L::kDu + t * 2 * CT + 2 * ic + 2, gB);
+#pragma unroll
+      for (int j = 0; j < VEC; j += 2)
+        load_pair_sums(sm + L::kDu + t * L::kRow + du_entry<2>(ic + j), gA + j, gB + j);
       load_vec<float, VEC>(sm + L::kDy + t * CT + ic, y);
       const int64_t at = (un.t0 + i * T + t) * a.D + col;
       float out[VEC];
@@ -459,9 +468,11 @@ __global__ void __launch_bounds__(Walk<S>::NT, Walk<S>::kCtas) scan_bwd_kernel(c
     fill_tile(i);
     __syncthreads();
     if (i > 0) copy_tile(i - 1);
-    if ((2 * i + 1) * kStep < len) walk(kStep, 2 * i + 1);
-    else copy_kept(2 * i - 1);
-    walk(0, 2 * i);
+#pragma unroll 1
+    for (int step = 2 * i + 1; step >= 2 * i; --step) {
+      if (step * kStep < len) walk((step & 1) * kStep, step);
+      else copy_kept(step - 2);
+    }
     __syncthreads();
     finish_tile(i);
     __syncthreads();  // the warps' sums have been read
