@@ -14,7 +14,7 @@ namespace kda {
 namespace {
 
 constexpr int kConvThreads = 256;
-constexpr int kUnroll = 8;  // rows in flight per thread
+constexpr int kUnroll = 4;  // rows per step; the next step's are in flight
 constexpr int kFV = 4;      // channels per thread of the prompt kernel
 
 // ------------------------------------------------------------ packed batch
@@ -222,7 +222,7 @@ __device__ __forceinline__ void store_final(const ConvArgs& a, int64_t item) {
 // would double the window and tap registers and halve the warps in flight
 // (bf16 at W = 4: 506 us instead of KERNEL_US at 65,000 x 4096).
 template <typename Tin, int W>
-__global__ void __launch_bounds__(kConvThreads, 3) conv_fwd_kernel(const ConvArgs a,
+__global__ void __launch_bounds__(kConvThreads, sizeof(Tin) == 4 ? 2 : 3) conv_fwd_kernel(const ConvArgs a,
                                                                    unsigned strip_blocks) {
   constexpr int V = kFV;
   if (a.cu) {
@@ -249,22 +249,35 @@ __global__ void __launch_bounds__(kConvThreads, 3) conv_fwd_kernel(const ConvArg
   load_taps<W, V>(a, c, w, b);
   Run r = run_at(a, t0);
   fill_window<Tin, W, V>(a, r, t0, c, win);
-  for (int t = t0; t < t1; t += kUnroll) {
-    float row[kUnroll][V];
-    const bool whole = t + kUnroll <= t1 && t + kUnroll <= r.end;
-    if (whole) {
+  // one token whose row is given
+  auto token = [&](const float (&row)[V], Tin* to) {
+    float p[V];
+    taps_dot<W, V>(w, b, win, row, p);
+    if (a.silu) {
 #pragma unroll
-      for (int u = 0; u < kUnroll; ++u) load_vec<Tin, V>(x + u * a.x_stride, row[u]);
+      for (int i = 0; i < V; ++i) p[i] *= sigmoid_fast(p[i]);
+    }
+    store_vec<V>(to, p);
+    push_row<W, V>(win, row);
+  };
+  Raw<Tin, V> next[kUnroll];
+  auto fetch = [&](int t) {  // the kUnroll rows from t on
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u)
+      if (t + u < t1) next[u].load(x + (int64_t)(t + u - t0) * a.x_stride);
+  };
+  fetch(t0);
+  for (int t = t0; t < t1; t += kUnroll) {
+    Raw<Tin, V> cur[kUnroll];
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u) cur[u] = next[u];
+    fetch(t + kUnroll);  // in flight while these are worked on
+    float row[V];
+    if (t + kUnroll <= t1 && t + kUnroll <= r.end) {
 #pragma unroll
       for (int u = 0; u < kUnroll; ++u) {
-        float p[V];
-        taps_dot<W, V>(w, b, win, row[u], p);
-        if (a.silu) {
-#pragma unroll
-          for (int i = 0; i < V; ++i) p[i] *= sigmoid_fast(p[i]);
-        }
-        store_vec<V>(out + (int64_t)u * a.D, p);
-        push_row<W, V>(win, row[u]);
+        cur[u].get(row);
+        token(row, out + (int64_t)u * a.D);
       }
     } else {
       for (int u = 0; u < kUnroll && t + u < t1; ++u) {
@@ -272,18 +285,10 @@ __global__ void __launch_bounds__(kConvThreads, 3) conv_fwd_kernel(const ConvArg
           r = run_at(a, t + u);
           fill_window<Tin, W, V>(a, r, t + u, c, win);
         }
-        float p[V];
-        load_vec<Tin, V>(x + u * a.x_stride, row[0]);
-        taps_dot<W, V>(w, b, win, row[0], p);
-        if (a.silu) {
-#pragma unroll
-          for (int i = 0; i < V; ++i) p[i] *= sigmoid_fast(p[i]);
-        }
-        store_vec<V>(out + (int64_t)u * a.D, p);
-        push_row<W, V>(win, row[0]);
+        load_vec<Tin, V>(x + (int64_t)(t + u - t0) * a.x_stride, row);
+        token(row, out + (int64_t)u * a.D);
       }
     }
-    x += kUnroll * a.x_stride;
     out += (int64_t)kUnroll * a.D;
   }
 }
@@ -340,7 +345,7 @@ constexpr int kBV = 2;  // channels per thread
 constexpr int kBU = 4;  // tokens whose rows are in flight
 
 template <typename Tin, int W>
-__global__ void __launch_bounds__(kConvThreads, 3) conv_bwd_kernel(const ConvArgs a,
+__global__ void __launch_bounds__(kConvThreads, sizeof(Tin) == 4 ? 2 : 3) conv_bwd_kernel(const ConvArgs a,
                                                                    unsigned strip_blocks) {
   constexpr int V = kBV;
   if (a.cu) {
@@ -434,27 +439,42 @@ __global__ void __launch_bounds__(kConvThreads, 3) conv_bwd_kernel(const ConvArg
     };
     const Tin* xp = static_cast<const Tin*>(a.x) + (int64_t)ta * a.x_stride + c;
     const float* dp = a.dout + (int64_t)ta * a.D + c;
+    Raw<Tin, V> nx[kBU];
+    Raw<float, V> nd[kBU];
+    auto fetch = [&](int t) {
+#pragma unroll
+      for (int u = 0; u < kBU; ++u)
+        if (t + u < tb) {
+          nx[u].load(xp + (int64_t)(t + u - ta) * a.x_stride);
+          nd[u].load(dp + (int64_t)(t + u - ta) * a.D);
+        }
+    };
+    fetch(ta);
     // the run's tokens, then the W - 1 behind them
     for (int t = ta; t < tb; t += kBU) {
+      Raw<Tin, V> cx[kBU];
+      Raw<float, V> cd[kBU];
+#pragma unroll
+      for (int u = 0; u < kBU; ++u) {
+        cx[u] = nx[u];
+        cd[u] = nd[u];
+      }
+      fetch(t + kBU);  // in flight while these are worked on
+      float row[V], dout[V];
       if (t >= ta + W - 1 && t + kBU <= tb) {
-        float rows[kBU][V], dos[kBU][V];
 #pragma unroll
         for (int u = 0; u < kBU; ++u) {
-          load_vec<Tin, V>(xp + u * a.x_stride, rows[u]);
-          load_vec<float, V>(dp + (int64_t)u * a.D, dos[u]);
+          cx[u].get(row);
+          cd[u].get(dout);
+          token(t + u, row, dout, true, true);
         }
-#pragma unroll
-        for (int u = 0; u < kBU; ++u) token(t + u, rows[u], dos[u], true, true);
       } else {
         for (int u = 0; u < kBU && t + u < tb; ++u) {
-          float row[V], dout[V];
-          load_vec<Tin, V>(xp + u * a.x_stride, row);
-          load_vec<float, V>(dp + (int64_t)u * a.D, dout);
+          load_vec<Tin, V>(xp + (int64_t)(t + u - ta) * a.x_stride, row);
+          load_vec<float, V>(dp + (int64_t)(t + u - ta) * a.D, dout);
           token(t + u, row, dout, true, head || t + u - (W - 1) >= ta);
         }
       }
-      xp += kBU * a.x_stride;
-      dp += (int64_t)kBU * a.D;
     }
     for (int t = tb; t < tb + W - 1; ++t) {
       float row[V] = {}, dout[V] = {};

@@ -173,11 +173,59 @@ __device__ __forceinline__ void store_vec(__nv_bfloat16* p, const float (&v)[V])
   }
 }
 
-// 1 / (1 + e^-x): e^-x = inf gives 0, NaN stays NaN.  __expf and the fast
-// division are off by a few 2^-23 relative for |x| < 30, where the result is
-// not yet 0 or 1; a bf16 rounding is 2^-9.
-__device__ __forceinline__ float sigmoid_fast(float x) {
-  return __fdividef(1.0f, 1.0f + __expf(-x));
+constexpr float kLog2e = 1.4426950408889634f;
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
 }
+
+// 1 / (1 + e^-x): e^-x = inf gives 0, NaN stays NaN.  The exponential is off by
+// (2 + |x|) 2^-22 of itself at most and the reciprocal by 2^-23, which a bf16
+// rounding (2^-9) hides; where |x| is large the result is 0 or 1 anyway.
+__device__ __forceinline__ float sigmoid_fast(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(1.0f + ex2(-kLog2e * x)));
+  return y;
+}
+
+// -------------------------------------------------------------- raw values
+// V elements as they lie in memory, so that loads stay in flight until their
+// first use
+template <typename T, int V>
+struct Raw {
+  static constexpr int BYTES = V * (int)sizeof(T);
+  static constexpr int N = BYTES < 4 ? 1 : BYTES / 4;
+  uint32_t r[N];
+  __device__ __forceinline__ void zero() {
+#pragma unroll
+    for (int i = 0; i < N; ++i) r[i] = 0;
+  }
+  __device__ __forceinline__ void load(const T* p) {
+    if constexpr (BYTES == 2) {
+      r[0] = *reinterpret_cast<const unsigned short*>(p);
+    } else if constexpr (BYTES == 4) {
+      r[0] = *reinterpret_cast<const uint32_t*>(p);
+    } else if constexpr (BYTES == 8) {
+      const uint2 u = *reinterpret_cast<const uint2*>(p);
+      r[0] = u.x; r[1] = u.y;
+    } else {
+#pragma unroll
+      for (int i = 0; i < N; i += 4) {
+        const uint4 u = reinterpret_cast<const uint4*>(p)[i / 4];
+        r[i] = u.x; r[i + 1] = u.y; r[i + 2] = u.z; r[i + 3] = u.w;
+      }
+    }
+  }
+  __device__ __forceinline__ void get(float (&v)[V]) const {
+#pragma unroll
+    for (int i = 0; i < V; ++i) v[i] = at(i);
+  }
+  __device__ __forceinline__ float at(int i) const {
+    if constexpr (sizeof(T) == 4) return __uint_as_float(r[i]);
+    else return __uint_as_float(i & 1 ? r[i >> 1] & 0xffff0000u : r[i >> 1] << 16);
+  }
+};
 
 }  // namespace kda

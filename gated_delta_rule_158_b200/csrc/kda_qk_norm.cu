@@ -21,7 +21,10 @@ namespace kda {
 namespace {
 
 constexpr int kNormThreads = 256;
-constexpr int kRowsInFlight = 4;  // rows per lane group and step
+// rows per lane group and step: 64 bytes in flight a lane
+template <typename Tin>
+constexpr int kRows = 8 / (int)sizeof(Tin);
+constexpr int kRowsInFlight = 4;
 constexpr int kMaxTokens = 16;    // tokens per block (shared table: 16 x 256 floats)
 
 struct NormArgs {
@@ -127,57 +130,73 @@ __device__ __forceinline__ int64_t dense_row(const NormArgs& a, int64_t t, const
   return r.isq ? (t * a.Hq + r.head) * a.d : (t * a.Hk + r.head - a.Hq) * a.d;
 }
 
+// Blocks walk over tiles of per_block tokens; the next step's rows (of this tile
+// or the next) are in flight while a step's are worked on.
 template <typename Tin, int L, int ROT>
 __global__ void __launch_bounds__(kNormThreads, 4) qk_norm_fwd_kernel(const NormArgs a) {
   extern __shared__ float2 tab[];
   constexpr int G = kNormThreads / L;  // lane groups
+  constexpr int U = kRows<Tin>;
   const int l = threadIdx.x % L, grp = threadIdx.x / L;
   const bool act = 8 * l < a.d;
-  const int t0 = blockIdx.x * a.per_block;
-  const int nt = min(a.per_block, a.tokens - t0);
-  const int H = a.Hq + a.Hk, rows = nt * H;
-  bool filled = ROT == kNoRot;
-  const int steps = (rows + G * kRowsInFlight - 1) / (G * kRowsInFlight);
-  for (int s0 = 0; s0 < steps; ++s0) {
-    float x[kRowsInFlight][8];
-    Row r[kRowsInFlight];
+  const int H = a.Hq + a.Hk;
+  const int steps = (a.per_block * H + G * U - 1) / (G * U);  // of a whole tile
+  const int tiles = (int)(((int64_t)a.tokens + a.per_block - 1) / a.per_block);
+  Raw<Tin, 8> next[U];
+  auto fetch = [&](int tile, int s) {
+    const int t0 = tile * a.per_block;
+    const int rows = min(a.per_block, a.tokens - t0) * H;
 #pragma unroll
-    for (int u = 0; u < kRowsInFlight; ++u) {
-      const int row = (s0 * kRowsInFlight + u) * G + grp;
-      r[u] = row_of(a, row, H);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) x[u][i] = 0.f;
-      if (row < rows && act)
-        load_vec<Tin, 8>(in_row<Tin>(a, t0 + r[u].tok, r[u]) + 8 * l, x[u]);
+    for (int u = 0; u < U; ++u) {
+      const int row = (s * U + u) * G + grp;
+      next[u].zero();
+      if (row < rows && act) {
+        const Row r = row_of(a, row, H);
+        next[u].load(in_row<Tin>(a, t0 + r.tok, r) + 8 * l);
+      }
     }
-    if (!filled) {
+  };
+  if ((int)blockIdx.x < tiles) fetch(blockIdx.x, 0);
+  for (int tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
+    const int t0 = tile * a.per_block;
+    const int nt = min(a.per_block, a.tokens - t0), rows = nt * H;
+    if (ROT != kNoRot) {
+      if (tile != (int)blockIdx.x) __syncthreads();  // the last tile's table has been read
       fill_turns(a, t0, nt, tab);
       __syncthreads();
-      filled = true;
     }
+    for (int s = 0; s < steps; ++s) {
+      Raw<Tin, 8> cur[U];
 #pragma unroll
-    for (int u = 0; u < kRowsInFlight; ++u) {
-      const int row = (s0 * kRowsInFlight + u) * G + grp;
-      float ss = 0.f;
+      for (int u = 0; u < U; ++u) cur[u] = next[u];
+      if (s + 1 < steps) fetch(tile, s + 1);
+      else if (tile + (int)gridDim.x < tiles) fetch(tile + gridDim.x, 0);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) ss = fmaf(x[u][i], x[u][i], ss);
-      const float f = rsqrtf(fmaf(a.c, group_sum<L>(ss), a.eps));
-      const float* wp = r[u].isq ? a.q_weight : a.k_weight;
-      if (wp && act) {
-        float w[8];
-        load_vec<float, 8>(wp + 8 * l, w);
+      for (int u = 0; u < U; ++u) {
+        const int row = (s * U + u) * G + grp;
+        const Row r = row_of(a, row, H);
+        float x[8], ss = 0.f;
+        cur[u].get(x);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) x[u][i] *= f * w[i];
-      } else {
+        for (int i = 0; i < 8; ++i) ss = fmaf(x[i], x[i], ss);
+        const float f = rsqrtf(fmaf(a.c, group_sum<L>(ss), a.eps));
+        const float* wp = r.isq ? a.q_weight : a.k_weight;
+        if (wp && act) {
+          float w[8];
+          load_vec<float, 8>(wp + 8 * l, w);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) x[u][i] *= f;
+          for (int i = 0; i < 8; ++i) x[i] *= f * w[i];
+        } else {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) x[i] *= f;
+        }
+        // rows past the end turn by the table's first token; nothing is stored
+        if (ROT != kNoRot)
+          turn<L, ROT>(a, tab + (row < rows ? r.tok : 0) * (a.rot >> 1), l, 1.f, x);
+        if (row < rows && act)
+          store_vec<8>(static_cast<Tin*>(r.isq ? a.q_out : a.k_out) +
+                           dense_row(a, t0 + r.tok, r) + 8 * l, x);
       }
-      // rows past the end turn by the table's first token; nothing is stored
-      if (ROT != kNoRot)
-        turn<L, ROT>(a, tab + (row < rows ? r[u].tok : 0) * (a.rot >> 1), l, 1.f, x[u]);
-      if (row < rows && act)
-        store_vec<8>(static_cast<Tin*>(r[u].isq ? a.q_out : a.k_out) +
-                         dense_row(a, t0 + r[u].tok, r[u]) + 8 * l, x[u]);
     }
   }
 }
@@ -186,78 +205,92 @@ __global__ void __launch_bounds__(kNormThreads, 4) qk_norm_fwd_kernel(const Norm
 // rows of its group) stays in registers over the walk, is added over the
 // block's groups in order, and leaves as one partial row per block.
 template <typename Tin, int L, int ROT>
-__global__ void __launch_bounds__(kNormThreads, 3) qk_norm_bwd_kernel(const NormArgs a) {
+__global__ void __launch_bounds__(kNormThreads, 2) qk_norm_bwd_kernel(const NormArgs a) {
   extern __shared__ float2 tab[];
   constexpr int G = kNormThreads / L;
   constexpr int U = 2;
   const int l = threadIdx.x % L, grp = threadIdx.x / L;
   const bool act = 8 * l < a.d;
   const int H = a.Hq + a.Hk;
+  const int steps = (a.per_block * H + G * U - 1) / (G * U);  // of a whole tile
+  const int tiles = (int)(((int64_t)a.tokens + a.per_block - 1) / a.per_block);
   float gq[8], gk[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) gq[i] = gk[i] = 0.f;
-  for (int64_t t0 = (int64_t)blockIdx.x * a.per_block; t0 < a.tokens;
-       t0 += (int64_t)a.blocks * a.per_block) {
-    const int nt = (int)min((int64_t)a.per_block, a.tokens - t0);
-    const int rows = nt * H;
-    const int steps = (rows + G * U - 1) / (G * U);
+  Raw<Tin, 8> nx[U];
+  Raw<float, 8> nd[U];
+  auto fetch = [&](int tile, int s) {
+    const int t0 = tile * a.per_block;
+    const int rows = min(a.per_block, a.tokens - t0) * H;
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int row = (s * U + u) * G + grp;
+      nx[u].zero();
+      nd[u].zero();
+      if (row < rows && act) {
+        const Row r = row_of(a, row, H);
+        nx[u].load(in_row<Tin>(a, t0 + r.tok, r) + 8 * l);
+        nd[u].load((r.isq ? a.dq_out : a.dk_out) + dense_row(a, t0 + r.tok, r) + 8 * l);
+      }
+    }
+  };
+  if ((int)blockIdx.x < tiles) fetch(blockIdx.x, 0);
+  for (int tile = blockIdx.x; tile < tiles; tile += a.blocks) {
+    const int t0 = tile * a.per_block;
+    const int nt = min(a.per_block, a.tokens - t0), rows = nt * H;
     if (ROT != kNoRot) {
-      __syncthreads();  // the last tile's table has been read
-      fill_turns(a, (int)t0, nt, tab);
+      if (tile != (int)blockIdx.x) __syncthreads();  // the last tile's table has been read
+      fill_turns(a, t0, nt, tab);
       __syncthreads();
     }
-    for (int s0 = 0; s0 < steps; ++s0) {
-      float x[U][8], dy[U][8];
-      Row r[U];
+    for (int s = 0; s < steps; ++s) {
+      Raw<Tin, 8> cx[U];
+      Raw<float, 8> cd[U];
 #pragma unroll
       for (int u = 0; u < U; ++u) {
-        const int row = (s0 * U + u) * G + grp;
-        r[u] = row_of(a, row, H);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) x[u][i] = dy[u][i] = 0.f;
-        if (row < rows && act) {
-          const int64_t t = t0 + r[u].tok;
-          load_vec<Tin, 8>(in_row<Tin>(a, t, r[u]) + 8 * l, x[u]);
-          load_vec<float, 8>((r[u].isq ? a.dq_out : a.dk_out) + dense_row(a, t, r[u]) + 8 * l,
-                             dy[u]);
-        }
+        cx[u] = nx[u];
+        cd[u] = nd[u];
       }
+      if (s + 1 < steps) fetch(tile, s + 1);
+      else if (tile + a.blocks < tiles) fetch(tile + a.blocks, 0);
 #pragma unroll
       for (int u = 0; u < U; ++u) {
-        const int row = (s0 * U + u) * G + grp;
-        float ss = 0.f;
+        const int row = (s * U + u) * G + grp;
+        const Row r = row_of(a, row, H);
+        float x[8], dy[8], ss = 0.f;
+        cx[u].get(x);
+        cd[u].get(dy);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) ss = fmaf(x[u][i], x[u][i], ss);
+        for (int i = 0; i < 8; ++i) ss = fmaf(x[i], x[i], ss);
         const float f = rsqrtf(fmaf(a.c, group_sum<L>(ss), a.eps));
         if (ROT != kNoRot)
-          turn<L, ROT>(a, tab + (row < rows ? r[u].tok : 0) * (a.rot >> 1), l, -1.f, dy[u]);
+          turn<L, ROT>(a, tab + (row < rows ? r.tok : 0) * (a.rot >> 1), l, -1.f, dy);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) x[u][i] *= f;
+        for (int i = 0; i < 8; ++i) x[i] *= f;
         if (a.partial) {  // rows past the end are zero
-          if (r[u].isq) {
+          if (r.isq) {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) gq[i] = fmaf(dy[u][i], x[u][i], gq[i]);
+            for (int i = 0; i < 8; ++i) gq[i] = fmaf(dy[i], x[i], gq[i]);
           } else {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) gk[i] = fmaf(dy[u][i], x[u][i], gk[i]);
+            for (int i = 0; i < 8; ++i) gk[i] = fmaf(dy[i], x[i], gk[i]);
           }
         }
-        const float* wp = r[u].isq ? a.q_weight : a.k_weight;
+        const float* wp = r.isq ? a.q_weight : a.k_weight;
         if (wp && act) {
           float w[8];
           load_vec<float, 8>(wp + 8 * l, w);
 #pragma unroll
-          for (int i = 0; i < 8; ++i) dy[u][i] *= w[i];
+          for (int i = 0; i < 8; ++i) dy[i] *= w[i];
         }
         float m = 0.f;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) m = fmaf(dy[u][i], x[u][i], m);
+        for (int i = 0; i < 8; ++i) m = fmaf(dy[i], x[i], m);
         m = a.c * group_sum<L>(m);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) dy[u][i] = f * fmaf(-x[u][i], m, dy[u][i]);
+        for (int i = 0; i < 8; ++i) dy[i] = f * fmaf(-x[i], m, dy[i]);
         if (row < rows && act)
-          store_vec<8>((r[u].isq ? a.dq : a.dk) + dense_row(a, t0 + r[u].tok, r[u]) + 8 * l,
-                       dy[u]);
+          store_vec<8>((r.isq ? a.dq : a.dk) + dense_row(a, t0 + r.tok, r) + 8 * l, dy);
       }
     }
   }
@@ -302,7 +335,7 @@ __global__ void __launch_bounds__(256) qk_norm_bwd_sum_kernel(const float* __res
 
 int lane_group(int d) { return d <= 32 ? 4 : d <= 64 ? 8 : d <= 128 ? 16 : 32; }
 
-// Tokens per block: enough rows for kRowsInFlight per lane group; with a
+// Tokens per tile: enough rows for kRowsInFlight per lane group; with a
 // rotation more, so that the block's threads form the angles of several tokens
 // at once (a token's 32 to 128 angles alone leave most of them waiting), as
 // long as every SM has four blocks.
@@ -318,7 +351,7 @@ int tokens_per_block(int tokens, int H, int d, int rot) {
   return n < 1 ? 1 : n;
 }
 
-constexpr int kBwdBlocks = 148 * 6;
+constexpr int kFwdBlocks = 148 * 4, kBwdBlocks = 148 * 2;  // as many as are resident
 int bwd_blocks(int tokens, int per_block) {
   const int64_t n = ((int64_t)tokens + per_block - 1) / per_block;
   return (int)(n < kBwdBlocks ? n : kBwdBlocks);
@@ -328,7 +361,8 @@ size_t table_bytes(const NormArgs& a) { return sizeof(float2) * (size_t)a.per_bl
 
 template <typename Tin, int ROT>
 cudaError_t dispatch_fwd_rot(const NormArgs& a, cudaStream_t st) {
-  const unsigned grid = (unsigned)(((int64_t)a.tokens + a.per_block - 1) / a.per_block);
+  const int64_t tiles = ((int64_t)a.tokens + a.per_block - 1) / a.per_block;
+  const unsigned grid = (unsigned)(tiles < kFwdBlocks ? tiles : kFwdBlocks);
   const size_t sm = table_bytes(a);
   switch (lane_group(a.d)) {
     case 4: qk_norm_fwd_kernel<Tin, 4, ROT><<<grid, kNormThreads, sm, st>>>(a); break;

@@ -195,7 +195,7 @@ __global__ void __launch_bounds__(Layout<S, SC_>::NT) scan_fwd_kernel(const Args
         if (a.z) {
           read_slot<Tin, VEC>(slot(i, 2, m), z);
 #pragma unroll
-          for (int j = 0; j < VEC; ++j) dy[j] *= z[j] * sigmoid2(z[j]);
+          for (int j = 0; j < VEC; ++j) dy[j] *= z[j] * sigmoid_fast(z[j]);
         }
         store_vec<VEC>(sm + M::kDy + t * CT + ic, dy);
       }
@@ -313,7 +313,7 @@ __global__ void __launch_bounds__(Layout<S, SC_>::NT) scan_fwd_kernel(const Args
 #pragma unroll
         for (int j = 0; j < VEC; ++j) {
           y[j] = fmaf(skip[j], x[j], y[j]);
-          if (a.z) y[j] *= z[j] * sigmoid2(z[j]);
+          if (a.z) y[j] *= z[j] * sigmoid_fast(z[j]);
         }
         store_vec<VEC>(static_cast<Tin*>(a.out) + (row0 + i * kTile + t) * a.D + col, y);
       }
@@ -490,7 +490,7 @@ __global__ void __launch_bounds__(256) scan_step_kernel(const Args a, float* sta
   }
   if (mine && nl < NSEQ) {
     if (a.D_skip) out = fmaf(a.D_skip[d], x, out);
-    if (a.z) out *= z * sigmoid2(z);
+    if (a.z) out *= z * sigmoid_fast(z);
     Elem<Tin>::store(static_cast<Tin*>(a.out) + (n0 + own) * a.D + d, out);
   }
 }

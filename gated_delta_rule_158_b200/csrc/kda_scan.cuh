@@ -7,8 +7,6 @@
 namespace kda {
 namespace scan {
 
-constexpr float kLog2e = 1.4426950408889634f;
-
 // The tokens are one flat axis; a unit is one segment (at most seg_len tokens)
 // of one sequence.  Dense: segs units per sequence.  Packed: the plan kernel
 // has chosen seg_len (in the status block) and written seg_off[n], the units
@@ -119,12 +117,6 @@ __device__ __forceinline__ Channels channels_of(const Args& a, int cb) {
 inline int channel_blocks(int D, int G, int CT) { return G * ((D / G + CT - 1) / CT); }
 
 // ------------------------------------------------------------- arithmetic
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-
 // two fp32 values side by side, one instruction for both
 using f2 = unsigned long long;
 __device__ __forceinline__ f2 pack2(float a, float b) {
@@ -211,10 +203,6 @@ __device__ __forceinline__ void step_sizes(float (&v)[V], bool softplus) {
   }
 }
 
-__device__ __forceinline__ float sigmoid2(float x) {
-  return __fdividef(1.0f, 1.0f + ex2(-kLog2e * x));
-}
-
 // ------------------------------------------------------- asynchronous copies
 // BYTES (4, 8, 16 or 32) from global to shared memory without registers; zeros
 // where !in (the source is not read then)
@@ -243,40 +231,6 @@ template <typename T, int V>
 __device__ __forceinline__ void read_slot(const char* p, float (&v)[V]) {
   load_vec<T, V>(reinterpret_cast<const T*>(p), v);
 }
-
-// -------------------------------------------------------------- raw values
-// V elements as they lie in memory, so that loads stay in flight until their
-// first use
-template <typename T, int V>
-struct Raw {
-  static constexpr int BYTES = V * (int)sizeof(T);
-  static constexpr int N = BYTES < 4 ? 1 : BYTES / 4;
-  uint32_t r[N];
-  __device__ __forceinline__ void zero() {
-#pragma unroll
-    for (int i = 0; i < N; ++i) r[i] = 0;
-  }
-  __device__ __forceinline__ void load(const T* p) {
-    if constexpr (BYTES == 2) {
-      r[0] = *reinterpret_cast<const unsigned short*>(p);
-    } else if constexpr (BYTES == 4) {
-      r[0] = *reinterpret_cast<const uint32_t*>(p);
-    } else if constexpr (BYTES == 8) {
-      const uint2 u = *reinterpret_cast<const uint2*>(p);
-      r[0] = u.x; r[1] = u.y;
-    } else {
-#pragma unroll
-      for (int i = 0; i < N; i += 4) {
-        const uint4 u = reinterpret_cast<const uint4*>(p)[i / 4];
-        r[i] = u.x; r[i + 1] = u.y; r[i + 2] = u.z; r[i + 3] = u.w;
-      }
-    }
-  }
-  __device__ __forceinline__ float at(int i) const {
-    if constexpr (sizeof(T) == 4) return __uint_as_float(r[i]);
-    else return __uint_as_float(i & 1 ? r[i >> 1] & 0xffff0000u : r[i >> 1] << 16);
-  }
-};
 
 // Sums of four tokens' values over the LN lanes of a channel.  LN >= 4: lane
 // l & 3 returns token l & 3; LN = 2: lane l returns tokens 2 l and 2 l + 1.

@@ -263,7 +263,7 @@ __global__ void __launch_bounds__(Walk<S>::NT, Walk<S>::kCtas) scan_bwd_kernel(c
         if (a.z) {
           read_slot<Tin, VEC>(slot(i, 2, m), z);
 #pragma unroll
-          for (int j = 0; j < VEC; ++j) dy[j] *= z[j] * sigmoid2(z[j]);
+          for (int j = 0; j < VEC; ++j) dy[j] *= z[j] * sigmoid_fast(z[j]);
         }
         store_du<2, VEC>(sm + L::kDu + t * L::kRow, ic, dt, u);
         store_vec<VEC>(sm + L::kDy + t * CT + ic, dy);
@@ -424,7 +424,7 @@ __global__ void __launch_bounds__(Walk<S>::NT, Walk<S>::kCtas) scan_bwd_kernel(c
 #pragma unroll
       for (int j = 0; j < VEC; ++j) {
         if (a.z) {
-          const float s = sigmoid2(z[j]), zs = z[j] * s;
+          const float s = sigmoid_fast(z[j]), zs = z[j] * s;
           out[j] = dy[j] * fmaf(skip[j], x[j], y[j]) * fmaf(zs, 1.f - s, s);
           dy[j] *= zs;
         }
@@ -437,7 +437,7 @@ __global__ void __launch_bounds__(Walk<S>::NT, Walk<S>::kCtas) scan_bwd_kernel(c
 #pragma unroll
       for (int j = 0; j < VEC; ++j) {
         out[j] = fmaf(gB[j], x[j], gA[j] * (1.f / kLog2e));
-        if (a.softplus) out[j] *= sigmoid2(v[j] + bias[j]);
+        if (a.softplus) out[j] *= sigmoid_fast(v[j] + bias[j]);
         sum_b[j] += out[j];
       }
       store_vec<VEC>(a.ddelta + at, out);
