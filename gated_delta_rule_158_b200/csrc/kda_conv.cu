@@ -14,8 +14,9 @@ namespace kda {
 namespace {
 
 constexpr int kConvThreads = 256;
-constexpr int kUnroll = 4;  // rows per step; the next step's are in flight
-constexpr int kFV = 4;      // channels per thread of the prompt kernel
+constexpr int kUnroll = 4;   // rows per step
+constexpr int kRing = 16;    // rows of a thread's ring
+constexpr int kFV = 4;       // channels per thread of the step kernel
 
 // ------------------------------------------------------------ packed batch
 __global__ void seqlens_plan_kernel(const int32_t* __restrict__ cu, int N, int T,
@@ -116,49 +117,70 @@ __device__ __forceinline__ Run run_at(const ConvArgs& a, int t) {
   return r;
 }
 
+// Rows of V channels as V / 2 pairs.
+template <typename Tin, int V>
+__device__ __forceinline__ void load_row(const Tin* p, f2 (&v)[V / 2]) {
+  float f[V];
+  load_vec<Tin, V>(p, f);
+#pragma unroll
+  for (int i = 0; i < V / 2; ++i) v[i] = pack2(f[2 * i], f[2 * i + 1]);
+}
+template <int V, typename T>
+__device__ __forceinline__ void store_row(T* p, const f2 (&v)[V / 2]) {
+  float f[V];
+#pragma unroll
+  for (int i = 0; i < V / 2; ++i) unpack2(v[i], f[2 * i], f[2 * i + 1]);
+  store_vec<V>(p, f);
+}
+template <typename T, int V>
+__device__ __forceinline__ void raw_row(const Raw<T, V>& r, f2 (&v)[V / 2]) {
+#pragma unroll
+  for (int i = 0; i < V / 2; ++i) v[i] = pack2(r.at(2 * i), r.at(2 * i + 1));
+}
+
 // the row `back` places before the run's start (1 = the newest kept row)
 template <typename Tin, int W, int V>
 __device__ __forceinline__ void kept_row(const ConvArgs& a, int n, int back, int c,
-                                         float (&v)[V]) {
+                                         f2 (&v)[V / 2]) {
   if (a.init) {
-    load_vec<Tin, V>(static_cast<const Tin*>(a.init) +
+    load_row<Tin, V>(static_cast<const Tin*>(a.init) +
                          ((int64_t)n * (W - 1) + (W - 1 - back)) * a.D + c, v);
   } else {
 #pragma unroll
-    for (int i = 0; i < V; ++i) v[i] = 0.f;
+    for (int i = 0; i < V / 2; ++i) v[i] = zero2();
   }
 }
 
 // win = the W - 1 rows before token t of run r, oldest first
 template <typename Tin, int W, int V>
 __device__ __forceinline__ void fill_window(const ConvArgs& a, const Run& r, int t, int c,
-                                            float (&win)[W - 1][V]) {
+                                            f2 (*win)[V / 2]) {
 #pragma unroll
   for (int j = 0; j < W - 1; ++j) {
     const int s = t - (W - 1) + j;
     if (s >= r.start)
-      load_vec<Tin, V>(static_cast<const Tin*>(a.x) + (int64_t)s * a.x_stride + c, win[j]);
+      load_row<Tin, V>(static_cast<const Tin*>(a.x) + (int64_t)s * a.x_stride + c, win[j]);
     else
       kept_row<Tin, W, V>(a, r.n, r.start - s, c, win[j]);
   }
 }
 
-template <int W, int V>
-__device__ __forceinline__ void push_row(float (&win)[W - 1][V], const float (&row)[V]) {
+template <int W, int P>
+__device__ __forceinline__ void push_row(f2 (*win)[P], const f2 (&row)[P]) {
 #pragma unroll
   for (int j = 0; j + 1 < W - 1; ++j)
 #pragma unroll
-    for (int i = 0; i < V; ++i) win[j][i] = win[j + 1][i];
+    for (int i = 0; i < P; ++i) win[j][i] = win[j + 1][i];
 #pragma unroll
-  for (int i = 0; i < V; ++i) win[W - 2][i] = row[i];
+  for (int i = 0; i < P; ++i) win[W - 2][i] = row[i];
 }
 
 template <int W, int V>
-__device__ __forceinline__ void load_taps(const ConvArgs& a, int c, float (&w)[V][W],
-                                          float (&b)[V]) {
+__device__ __forceinline__ void load_taps(const ConvArgs& a, int c, f2 (&w)[W][V / 2],
+                                          f2 (&b)[V / 2]) {
   // V * W consecutive floats; c is a multiple of V, so V * W floats are a whole
   // number of 8- or 16-byte pieces
-  float flat[V * W];
+  float flat[V * W], bias[V] = {};
   constexpr int P = V * W % 4 == 0 ? 4 : 2;
 #pragma unroll
   for (int i = 0; i < V * W; i += P) {
@@ -167,29 +189,31 @@ __device__ __forceinline__ void load_taps(const ConvArgs& a, int c, float (&w)[V
 #pragma unroll
     for (int j = 0; j < P; ++j) flat[i + j] = f[j];
   }
+  if (a.bias) load_vec<float, V>(a.bias + c, bias);
 #pragma unroll
-  for (int i = 0; i < V; ++i)
+  for (int i = 0; i < V / 2; ++i) {
+    b[i] = pack2(bias[2 * i], bias[2 * i + 1]);
 #pragma unroll
-    for (int j = 0; j < W; ++j) w[i][j] = flat[i * W + j];
-  if (a.bias) {
-    load_vec<float, V>(a.bias + c, b);
-  } else {
-#pragma unroll
-    for (int i = 0; i < V; ++i) b[i] = 0.f;
+    for (int j = 0; j < W; ++j) w[j][i] = pack2(flat[2 * i * W + j], flat[(2 * i + 1) * W + j]);
   }
 }
 
-template <int W, int V>
-__device__ __forceinline__ void taps_dot(const float (&w)[V][W], const float (&b)[V],
-                                         const float (&win)[W - 1][V], const float (&row)[V],
-                                         float (&p)[V]) {
+// p = b + sum_j w[j] rows[j], rows[0] the oldest
+template <int W, int P, int N>
+__device__ __forceinline__ void taps_dot(const f2 (&w)[W][P], const f2 (&b)[P],
+                                         const f2 (&rows)[N][P], int first, f2 (&p)[P]) {
 #pragma unroll
-  for (int i = 0; i < V; ++i) {
-    float s = b[i];
+  for (int i = 0; i < P; ++i) {
+    p[i] = b[i];
 #pragma unroll
-    for (int j = 0; j < W - 1; ++j) s = fmaf(w[i][j], win[j][i], s);
-    p[i] = fmaf(w[i][W - 1], row[i], s);
+    for (int j = 0; j < W; ++j) p[i] = fma2(w[j][i], rows[first + j][i], p[i]);
   }
+}
+
+template <int P>
+__device__ __forceinline__ void silu_row(f2 (&p)[P]) {
+#pragma unroll
+  for (int i = 0; i < P; ++i) p[i] = mul2(p[i], sigmoid2(p[i]));
 }
 
 // rows of the final state: row j of sequence n is place len - (W-1) + j
@@ -209,22 +233,23 @@ __device__ __forceinline__ void store_final(const ConvArgs& a, int64_t item) {
     len = a.T;
   }
   const int64_t s = len - (W - 1) + j;
-  float v[V];
+  f2 v[V / 2];
   if (s >= 0)
-    load_vec<Tin, V>(static_cast<const Tin*>(a.x) + (start + s) * a.x_stride + c, v);
+    load_row<Tin, V>(static_cast<const Tin*>(a.x) + (start + s) * a.x_stride + c, v);
   else
     kept_row<Tin, W, V>(a, n, (int)-s, c, v);
-  store_vec<V>(static_cast<Tin*>(a.final_state) + r * a.D + c, v);  // exact: the type is the same
+  store_row<V>(static_cast<Tin*>(a.final_state) + r * a.D + c, v);  // exact: the type is the same
 }
 
 // Threads [0, strips * D / V) take a strip each, channel groups fastest; the
-// blocks behind them write the final state.  Four channels a thread: eight
-// would double the window and tap registers and halve the warps in flight
-// (bf16 at W = 4: 506 us instead of KERNEL_US at 65,000 x 4096).
+// blocks behind them write the final state.  A thread's rows come through a
+// ring of kRing rows in shared memory that it alone copies to and reads
+// (cp.async): 16 bytes x 12 to 16 rows in flight a thread, without a register.
 template <typename Tin, int W>
-__global__ void __launch_bounds__(kConvThreads, sizeof(Tin) == 4 ? 2 : 3) conv_fwd_kernel(const ConvArgs a,
+__global__ void __launch_bounds__(kConvThreads, 2) conv_fwd_kernel(const ConvArgs a,
                                                                    unsigned strip_blocks) {
-  constexpr int V = kFV;
+  constexpr int V = 16 / (int)sizeof(Tin), P = V / 2, U = kUnroll, GROUPS = kRing / U;
+  extern __shared__ __align__(16) char ring[];
   if (a.cu) {
     if (!a.sb->seqlens_ok) return;
   } else if (blockIdx.x == 0 && threadIdx.x == 0) {
@@ -244,52 +269,60 @@ __global__ void __launch_bounds__(kConvThreads, sizeof(Tin) == 4 ? 2 : 3) conv_f
   const int t1 = (int)min((int64_t)t0 + a.strip, a.total);
   const Tin* x = static_cast<const Tin*>(a.x) + (int64_t)t0 * a.x_stride + c;
   Tin* out = static_cast<Tin*>(a.out) + (int64_t)t0 * a.D + c;
+  char* const own = ring + threadIdx.x * 16;
+  auto copy_group = [&](int g) {
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int k = g * U + u;
+      if (t0 + k < t1)
+        copy_in<16>(own + (g % GROUPS * U + u) * kConvThreads * 16, x + (int64_t)k * a.x_stride,
+                    true);
+    }
+    copies_issued();
+  };
+#pragma unroll
+  for (int g = 0; g < GROUPS - 1; ++g) copy_group(g);
 
-  float w[V][W], b[V], win[W - 1][V];
+  f2 w[W][P], b[P];
+  f2 rows[W - 1 + U][P];  // the W - 1 rows before the step's tokens, then theirs
   load_taps<W, V>(a, c, w, b);
   Run r = run_at(a, t0);
-  fill_window<Tin, W, V>(a, r, t0, c, win);
-  // one token whose row is given
-  auto token = [&](const float (&row)[V], Tin* to) {
-    float p[V];
-    taps_dot<W, V>(w, b, win, row, p);
-    if (a.silu) {
+  fill_window<Tin, W, V>(a, r, t0, c, rows);
+  for (int t = t0, g = 0; t < t1; t += U, ++g) {
+    copy_group(g + GROUPS - 1);  // over the group that has been read
+    copies_landed_but<GROUPS - 1>();
+    const char* at = own + g % GROUPS * U * kConvThreads * 16;
+    if (t + U <= t1 && t + U <= r.end) {
 #pragma unroll
-      for (int i = 0; i < V; ++i) p[i] *= sigmoid_fast(p[i]);
-    }
-    store_vec<V>(to, p);
-    push_row<W, V>(win, row);
-  };
-  Raw<Tin, V> next[kUnroll];
-  auto fetch = [&](int t) {  // the kUnroll rows from t on
+      for (int u = 0; u < U; ++u)
+        load_row<Tin, V>(reinterpret_cast<const Tin*>(at + u * kConvThreads * 16),
+                         rows[W - 1 + u]);
 #pragma unroll
-    for (int u = 0; u < kUnroll; ++u)
-      if (t + u < t1) next[u].load(x + (int64_t)(t + u - t0) * a.x_stride);
-  };
-  fetch(t0);
-  for (int t = t0; t < t1; t += kUnroll) {
-    Raw<Tin, V> cur[kUnroll];
-#pragma unroll
-    for (int u = 0; u < kUnroll; ++u) cur[u] = next[u];
-    fetch(t + kUnroll);  // in flight while these are worked on
-    float row[V];
-    if (t + kUnroll <= t1 && t + kUnroll <= r.end) {
-#pragma unroll
-      for (int u = 0; u < kUnroll; ++u) {
-        cur[u].get(row);
-        token(row, out + (int64_t)u * a.D);
+      for (int u = 0; u < U; ++u) {
+        f2 p[P];
+        taps_dot<W, P>(w, b, rows, u, p);
+        if (a.silu) silu_row(p);
+        store_row<V>(out + (int64_t)u * a.D, p);
       }
+#pragma unroll
+      for (int j = 0; j < W - 1; ++j)
+#pragma unroll
+        for (int i = 0; i < P; ++i) rows[j][i] = rows[U + j][i];
     } else {
-      for (int u = 0; u < kUnroll && t + u < t1; ++u) {
+      for (int u = 0; u < U && t + u < t1; ++u) {
         if (t + u >= r.end) {  // the next sequence that has tokens
           r = run_at(a, t + u);
-          fill_window<Tin, W, V>(a, r, t + u, c, win);
+          fill_window<Tin, W, V>(a, r, t + u, c, rows);
         }
-        load_vec<Tin, V>(x + (int64_t)(t + u - t0) * a.x_stride, row);
-        token(row, out + (int64_t)u * a.D);
+        f2 p[P];
+        load_row<Tin, V>(reinterpret_cast<const Tin*>(at + u * kConvThreads * 16), rows[W - 1]);
+        taps_dot<W, P>(w, b, rows, 0, p);
+        if (a.silu) silu_row(p);
+        store_row<V>(out + (int64_t)u * a.D, p);
+        push_row<W, P>(rows, rows[W - 1]);
       }
     }
-    out += (int64_t)kUnroll * a.D;
+    out += (int64_t)U * a.D;
   }
 }
 
@@ -305,31 +338,28 @@ __global__ void __launch_bounds__(kConvThreads)
   const int64_t n0 = idx / CG * NS;
   if (n0 >= N) return;
   const int c = (int)(idx % CG) * V;
-  float w[V][W], b[V];
-  float win[NS][W - 1][V], row[NS][V];
+  constexpr int P = V / 2;
+  f2 w[W][P], b[P], rows[NS][W][P];
+  Raw<Tin, V> raw[NS][W];
 #pragma unroll
   for (int s = 0; s < NS; ++s) {
     if (n0 + s >= N) break;
-    load_vec<Tin, V>(static_cast<const Tin*>(a.x) + (n0 + s) * a.x_stride + c, row[s]);
 #pragma unroll
-    for (int j = 0; j < W - 1; ++j)
-      load_vec<Tin, V>(state + ((n0 + s) * (W - 1) + j) * a.D + c, win[s][j]);
+    for (int j = 0; j < W - 1; ++j) raw[s][j].load(state + ((n0 + s) * (W - 1) + j) * a.D + c);
+    raw[s][W - 1].load(static_cast<const Tin*>(a.x) + (n0 + s) * a.x_stride + c);
   }
   load_taps<W, V>(a, c, w, b);
 #pragma unroll
   for (int s = 0; s < NS; ++s) {
     if (n0 + s >= N) break;
-    float p[V];
-    taps_dot<W, V>(w, b, win[s], row[s], p);
-    if (a.silu) {
 #pragma unroll
-      for (int i = 0; i < V; ++i) p[i] *= sigmoid_fast(p[i]);
-    }
-    store_vec<V>(static_cast<Tin*>(a.out) + (n0 + s) * a.D + c, p);
-    push_row<W, V>(win[s], row[s]);
+    for (int j = 0; j < W; ++j) raw_row(raw[s][j], rows[s][j]);
+    f2 p[P];
+    taps_dot<W, P>(w, b, rows[s], 0, p);
+    if (a.silu) silu_row(p);
+    store_row<V>(static_cast<Tin*>(a.out) + (n0 + s) * a.D + c, p);
 #pragma unroll
-    for (int j = 0; j < W - 1; ++j)
-      store_vec<V>(state + ((n0 + s) * (W - 1) + j) * a.D + c, win[s][j]);
+    for (int j = 0; j < W - 1; ++j) raw[s][j + 1].store(state + ((n0 + s) * (W - 1) + j) * a.D + c);
   }
 }
 
@@ -341,11 +371,11 @@ __global__ void __launch_bounds__(kConvThreads)
 // the last W - 1 values of ds stays in registers.  dweight and dbias are
 // summed in registers over the strip's own tokens and leave as one partial
 // row per strip, added in strip order by conv_bwd_sum_kernel.
-constexpr int kBV = 2;  // channels per thread
-constexpr int kBU = 4;  // tokens whose rows are in flight
+constexpr int kBV = 4;     // channels per thread
+constexpr int kBRing = 12; // rows of a thread's ring
 
 template <typename Tin, int W>
-__global__ void __launch_bounds__(kConvThreads, sizeof(Tin) == 4 ? 2 : 3) conv_bwd_kernel(const ConvArgs a,
+__global__ void __launch_bounds__(kConvThreads, 2) conv_bwd_kernel(const ConvArgs a,
                                                                    unsigned strip_blocks) {
   constexpr int V = kBV;
   if (a.cu) {
@@ -374,128 +404,164 @@ __global__ void __launch_bounds__(kConvThreads, sizeof(Tin) == 4 ? 2 : 3) conv_b
   const int t0 = strip * a.strip;
   const int t1 = (int)min((int64_t)t0 + a.strip, a.total);
 
-  float w[V][W], b[V], win[W - 1][V], dsw[W - 1][V], dw[V][W], db[V];
+  constexpr int P = V / 2, U = kUnroll, GROUPS = kBRing / U;
+  // the thread's ring: of each row x, then dout
+  constexpr int XB = V * (int)sizeof(Tin), DB = V * 4;
+  extern __shared__ __align__(16) char ring[];
+  char* const own_x = ring + threadIdx.x * XB;
+  char* const own_d = ring + kBRing * kConvThreads * XB + threadIdx.x * DB;
+  const Tin* xs = static_cast<const Tin*>(a.x) + (int64_t)t0 * a.x_stride + c;
+  const float* dsrc = a.dout + (int64_t)t0 * a.D + c;
+  auto copy_group = [&](int g) {
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int k = g * U + u, at = (g % GROUPS * U + u) * kConvThreads;
+      if (t0 + k < t1) {
+        copy_in<XB>(own_x + at * XB, xs + (int64_t)k * a.x_stride, true);
+        copy_in<DB>(own_d + at * DB, dsrc + (int64_t)k * a.D, true);
+      }
+    }
+    copies_issued();
+  };
+#pragma unroll
+  for (int g = 0; g < GROUPS - 1; ++g) copy_group(g);
+  f2 w[W][P], b[P], dw[W][P], db[P];
+  // the W - 1 rows (and values of ds) before the step's tokens, then theirs
+  f2 rows[W - 1 + U][P], dss[W - 1 + U][P];
   load_taps<W, V>(a, c, w, b);
 #pragma unroll
-  for (int i = 0; i < V; ++i) {
-    db[i] = 0.f;
+  for (int i = 0; i < P; ++i) {
+    db[i] = zero2();
 #pragma unroll
-    for (int j = 0; j < W; ++j) dw[i][j] = 0.f;
+    for (int j = 0; j < W; ++j) dw[j][i] = zero2();
   }
-  for (int ta = t0; ta < t1;) {
-    const Run r = run_at(a, ta);
-    const int tb = min(t1, r.end);
-    fill_window<Tin, W, V>(a, r, ta, c, win);
+  // ds of the token whose row is rows[u + W - 1], over its dout in dss[u + W - 1]
+  auto ds_of = [&](int u) {
+    if (!a.silu) return;
+    f2 p[P];
+    taps_dot<W, P>(w, b, rows, u, p);
+#pragma unroll
+    for (int i = 0; i < P; ++i) {  // silu'(p) = s + p s (1 - s)
+      const f2 s = sigmoid2(p[i]), ps = mul2(p[i], s);
+      dss[u + W - 1][i] = mul2(dss[u + W - 1][i], fma2(ps, fma2(s, pack2(-1.f, -1.f), pack2(1.f, 1.f)), s));
+    }
+  };
+  auto sums_of = [&](int u) {
+#pragma unroll
+    for (int i = 0; i < P; ++i) {
+      db[i] = add2(db[i], dss[u + W - 1][i]);
+#pragma unroll
+      for (int j = 0; j < W; ++j) dw[j][i] = fma2(dss[u + W - 1][i], rows[u + j][i], dw[j][i]);
+    }
+  };
+  // the gradient of the row W - 1 places before the token
+  auto row_gradient = [&](int u, f2 (&g)[P]) {
+#pragma unroll
+    for (int i = 0; i < P; ++i) {
+      g[i] = mul2(w[0][i], dss[u + W - 1][i]);
+#pragma unroll
+      for (int j = 1; j < W; ++j) g[i] = fma2(w[j][i], dss[u + W - 1 - j][i], g[i]);
+    }
+  };
+  Run r;
+  int ta, tb;  // the run's tokens within the strip
+  bool head;
+  auto start_run = [&](int t) {
+    r = run_at(a, t);
+    ta = t;
+    tb = min(t1, r.end);
+    head = ta == r.start && a.d_init;
+    fill_window<Tin, W, V>(a, r, ta, c, rows);
 #pragma unroll
     for (int j = 0; j < W - 1; ++j)
 #pragma unroll
-      for (int i = 0; i < V; ++i) dsw[j][i] = 0.f;
-    const bool head = ta == r.start && a.d_init;
-    // token t's ds from its rows, its sums; then the gradient of row t - (W-1)
-    auto token = [&](int t, const float (&row)[V], const float (&dout)[V], bool own, bool give) {
-      float ds[V];
+      for (int i = 0; i < P; ++i) dss[j][i] = zero2();
+  };
+  // token t alone, its row and dout in rows[W - 1] and dss[W - 1]
+  auto token = [&](int t, bool own) {
+    if (t < r.end) ds_of(0);
+    if (own) sums_of(0);
+    const int s = t - (W - 1);
+    if (s >= ta || head) {
+      f2 g[P];
+      row_gradient(0, g);
+      const int f = t - r.end;  // the row's place in the final state
+      if (f >= 0 && a.d_final) {
+        f2 d[P];
+        load_row<float, V>(a.d_final + ((int64_t)r.n * (W - 1) + f) * a.D + c, d);
 #pragma unroll
-      for (int i = 0; i < V; ++i) ds[i] = dout[i];
-      if (a.silu) {
-        float p[V];
-        taps_dot<W, V>(w, b, win, row, p);
-#pragma unroll
-        for (int i = 0; i < V; ++i) {
-          const float sg = sigmoid_fast(p[i]);
-          ds[i] *= sg * fmaf(p[i], 1.f - sg, 1.f);
-        }
+        for (int i = 0; i < P; ++i) g[i] = add2(g[i], d[i]);
       }
-      if (own) {
-#pragma unroll
-        for (int i = 0; i < V; ++i) {
-          db[i] += ds[i];
-#pragma unroll
-          for (int j = 0; j < W - 1; ++j) dw[i][j] = fmaf(ds[i], win[j][i], dw[i][j]);
-          dw[i][W - 1] = fmaf(ds[i], row[i], dw[i][W - 1]);
-        }
-      }
-      push_row<W, V>(win, row);
-      if (give) {
-        float g[V];
-#pragma unroll
-        for (int i = 0; i < V; ++i) {
-          g[i] = w[i][0] * ds[i];
-#pragma unroll
-          for (int j = 0; j < W - 1; ++j) g[i] = fmaf(w[i][W - 1 - j], dsw[j][i], g[i]);
-        }
-        const int s = t - (W - 1);
-        const int f = s - (r.end - (W - 1));  // its row of the final state
-        if (f >= 0 && a.d_final) {
-          float d[V];
-          load_vec<float, V>(a.d_final + ((int64_t)r.n * (W - 1) + f) * a.D + c, d);
-#pragma unroll
-          for (int i = 0; i < V; ++i) g[i] += d[i];
-        }
-        float* to = s >= ta ? a.dx + (int64_t)s * a.D
-                            : a.d_init + ((int64_t)r.n * (W - 1) + (s - ta + W - 1)) * a.D;
-        store_vec<V>(to + c, g);
-      }
-      push_row<W, V>(dsw, ds);
-    };
-    const Tin* xp = static_cast<const Tin*>(a.x) + (int64_t)ta * a.x_stride + c;
-    const float* dp = a.dout + (int64_t)ta * a.D + c;
-    Raw<Tin, V> nx[kBU];
-    Raw<float, V> nd[kBU];
-    auto fetch = [&](int t) {
-#pragma unroll
-      for (int u = 0; u < kBU; ++u)
-        if (t + u < tb) {
-          nx[u].load(xp + (int64_t)(t + u - ta) * a.x_stride);
-          nd[u].load(dp + (int64_t)(t + u - ta) * a.D);
-        }
-    };
-    fetch(ta);
-    // the run's tokens, then the W - 1 behind them
-    for (int t = ta; t < tb; t += kBU) {
-      Raw<Tin, V> cx[kBU];
-      Raw<float, V> cd[kBU];
-#pragma unroll
-      for (int u = 0; u < kBU; ++u) {
-        cx[u] = nx[u];
-        cd[u] = nd[u];
-      }
-      fetch(t + kBU);  // in flight while these are worked on
-      float row[V], dout[V];
-      if (t >= ta + W - 1 && t + kBU <= tb) {
-#pragma unroll
-        for (int u = 0; u < kBU; ++u) {
-          cx[u].get(row);
-          cd[u].get(dout);
-          token(t + u, row, dout, true, true);
-        }
-      } else {
-        for (int u = 0; u < kBU && t + u < tb; ++u) {
-          load_vec<Tin, V>(xp + (int64_t)(t + u - ta) * a.x_stride, row);
-          load_vec<float, V>(dp + (int64_t)(t + u - ta) * a.D, dout);
-          token(t + u, row, dout, true, head || t + u - (W - 1) >= ta);
-        }
-      }
+      float* to = s >= ta ? a.dx + (int64_t)s * a.D
+                          : a.d_init + ((int64_t)r.n * (W - 1) + (s - ta + W - 1)) * a.D;
+      store_row<V>(to + c, g);
     }
+    push_row<W, P>(rows, rows[W - 1]);
+    push_row<W, P>(dss, dss[W - 1]);
+  };
+  // the W - 1 tokens behind a run: the sequence's next ones (whose sums belong
+  // to the next strip), or none
+  auto end_run = [&]() {
     for (int t = tb; t < tb + W - 1; ++t) {
-      float row[V] = {}, dout[V] = {};
+#pragma unroll
+      for (int i = 0; i < P; ++i) rows[W - 1][i] = dss[W - 1][i] = zero2();
       if (t < r.end) {
-        load_vec<Tin, V>(static_cast<const Tin*>(a.x) + (int64_t)t * a.x_stride + c, row);
-        load_vec<float, V>(a.dout + (int64_t)t * a.D + c, dout);
+        load_row<Tin, V>(static_cast<const Tin*>(a.x) + (int64_t)t * a.x_stride + c, rows[W - 1]);
+        load_row<float, V>(a.dout + (int64_t)t * a.D + c, dss[W - 1]);
       }
-      token(t, row, dout, false, head || t - (W - 1) >= ta);
+      token(t, false);
     }
-    ta = tb;
+  };
+  start_run(t0);
+  float* gp = a.dx + (int64_t)t0 * a.D + c;
+  for (int t = t0, g = 0; t < t1; t += U, ++g) {
+    copy_group(g + GROUPS - 1);  // over the group that has been read
+    copies_landed_but<GROUPS - 1>();
+    const int at = g % GROUPS * U * kConvThreads;
+    if (t >= ta + W - 1 && t + U <= tb) {
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        load_row<Tin, V>(reinterpret_cast<const Tin*>(own_x + (at + u * kConvThreads) * XB),
+                         rows[W - 1 + u]);
+        load_row<float, V>(reinterpret_cast<const float*>(own_d + (at + u * kConvThreads) * DB),
+                           dss[W - 1 + u]);
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        f2 gr[P];
+        ds_of(u);
+        sums_of(u);
+        row_gradient(u, gr);
+        store_row<V>(gp + (int64_t)(u - (W - 1)) * a.D, gr);
+      }
+#pragma unroll
+      for (int j = 0; j < W - 1; ++j)
+#pragma unroll
+        for (int i = 0; i < P; ++i) {
+          rows[j][i] = rows[U + j][i];
+          dss[j][i] = dss[U + j][i];
+        }
+    } else {
+      for (int u = 0; u < U && t + u < t1; ++u) {
+        if (t + u >= tb) {
+          end_run();
+          start_run(t + u);
+        }
+        load_row<Tin, V>(reinterpret_cast<const Tin*>(own_x + (at + u * kConvThreads) * XB),
+                         rows[W - 1]);
+        load_row<float, V>(reinterpret_cast<const float*>(own_d + (at + u * kConvThreads) * DB),
+                           dss[W - 1]);
+        token(t + u, true);
+      }
+    }
+    gp += (int64_t)U * a.D;
   }
+  end_run();
   // [strip][W + 1][D]: tap j of all channels, then the bias
   float* part = a.partial + (int64_t)strip * (W + 1) * a.D + c;
 #pragma unroll
-  for (int j = 0; j < W; ++j) {
-    float v[V];
-#pragma unroll
-    for (int i = 0; i < V; ++i) v[i] = dw[i][j];
-    store_vec<V>(part + (int64_t)j * a.D, v);
-  }
-  store_vec<V>(part + (int64_t)W * a.D, db);
+  for (int j = 0; j < W; ++j) store_row<V>(part + (int64_t)j * a.D, dw[j]);
+  store_row<V>(part + (int64_t)W * a.D, db);
 }
 
 // Element e = (j, d) of the partial rows, added over the strips: eight threads
@@ -524,37 +590,46 @@ __global__ void __launch_bounds__(256) conv_bwd_sum_kernel(const float* __restri
   else if (dbias) dbias[d] = s;
 }
 
-// Tokens per strip: long strips read fewer head rows again and leave fewer
-// partial sums; strips are shortened (to `lo` at least) until the GPU has
-// `want` threads.
-int strip_len(int64_t total, int groups, int lo, int hi, int64_t want) {
-  int64_t s = total * groups / want;
-  s = s / 8 * 8;
-  if (s < lo) s = lo;
-  if (s > hi) s = hi;
-  return (int)s;
+// Tokens per strip.  Long strips read fewer head rows again and leave fewer
+// partial sums, but the strips have to fill the GPU evenly: 148 SMs hold two
+// blocks each, so the batch is cut into as many strips as fill one, two, ..
+// such waves, the fewest waves that keep a strip within `hi` tokens.
+int strip_len(int64_t total, int groups, int lo, int hi) {
+  int64_t per_wave = 148LL * 2 * kConvThreads / groups;
+  if (per_wave < 1) per_wave = 1;
+  int64_t waves = (total + per_wave * hi - 1) / (per_wave * hi);
+  int64_t s = (total + per_wave * waves - 1) / (per_wave * waves);
+  s = (s + 3) / 4 * 4;
+  return (int)(s < lo ? lo : s);
 }
 
-constexpr int64_t kWantThreads = 148LL * 1024;
+int bwd_strip(int64_t total, int D) { return strip_len(total, D / kBV, 16, 512); }
 
-int bwd_strip(int64_t total, int D) {
-  return strip_len(total, D / kBV, 16, 1 << 20, kWantThreads);
+// shared memory above the default needs the kernel's permission
+template <typename K>
+cudaError_t launch_ring(K kernel, const ConvArgs& a, int64_t blocks, int64_t more, size_t bytes,
+                        cudaStream_t st) {
+  if (bytes > 48 * 1024)
+    if (cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                             (int)bytes))
+      return e;
+  kernel<<<(unsigned)(blocks + more), kConvThreads, bytes, st>>>(a, (unsigned)blocks);
+  return cudaGetLastError();
 }
 
 template <typename Tin>
 cudaError_t dispatch_fwd(const ConvArgs& a, int W, cudaStream_t st) {
-  constexpr int V = kFV;
+  constexpr int V = 16 / (int)sizeof(Tin);
+  constexpr size_t bytes = (size_t)kRing * kConvThreads * 16;
   const int64_t blocks = ((int64_t)a.strips * (a.D / V) + kConvThreads - 1) / kConvThreads;
   int64_t fin = 0;
   if (a.final_state)
     fin = ((int64_t)a.num_seqs * (W - 1) * (a.D / V) + kConvThreads - 1) / kConvThreads;
-  const unsigned grid = (unsigned)(blocks + fin);
   switch (W) {
-    case 2: conv_fwd_kernel<Tin, 2><<<grid, kConvThreads, 0, st>>>(a, (unsigned)blocks); break;
-    case 3: conv_fwd_kernel<Tin, 3><<<grid, kConvThreads, 0, st>>>(a, (unsigned)blocks); break;
-    default: conv_fwd_kernel<Tin, 4><<<grid, kConvThreads, 0, st>>>(a, (unsigned)blocks); break;
+    case 2: return launch_ring(conv_fwd_kernel<Tin, 2>, a, blocks, fin, bytes, st);
+    case 3: return launch_ring(conv_fwd_kernel<Tin, 3>, a, blocks, fin, bytes, st);
+    default: return launch_ring(conv_fwd_kernel<Tin, 4>, a, blocks, fin, bytes, st);
   }
-  return cudaGetLastError();
 }
 
 template <typename Tin, int W>
@@ -563,7 +638,7 @@ cudaError_t launch_step(const ConvArgs& a, void* state, int N, cudaStream_t st) 
   Tin* sp = static_cast<Tin*>(state);
   constexpr int NS = 4;
   const int64_t few = ((int64_t)N + NS - 1) / NS * CG;  // threads with four sequences each
-  if (few >= kWantThreads / 2) {
+  if (few >= 148 * 512) {
     conv_step_kernel<Tin, W, NS>
         <<<(unsigned)((few + kConvThreads - 1) / kConvThreads), kConvThreads, 0, st>>>(a, sp, N);
   } else {
@@ -585,17 +660,16 @@ cudaError_t dispatch_step(const ConvArgs& a, void* state, int N, int W, cudaStre
 
 template <typename Tin>
 cudaError_t dispatch_bwd(const ConvArgs& a, int W, cudaStream_t st) {
+  constexpr size_t bytes = (size_t)kBRing * kConvThreads * kBV * (sizeof(Tin) + 4);
   const int64_t blocks = ((int64_t)a.strips * (a.D / kBV) + kConvThreads - 1) / kConvThreads;
   int64_t empty = 0;
   if (a.cu && a.d_init)
     empty = ((int64_t)a.num_seqs * (W - 1) * (a.D / kBV) + kConvThreads - 1) / kConvThreads;
-  const unsigned grid = (unsigned)(blocks + empty);
   switch (W) {
-    case 2: conv_bwd_kernel<Tin, 2><<<grid, kConvThreads, 0, st>>>(a, (unsigned)blocks); break;
-    case 3: conv_bwd_kernel<Tin, 3><<<grid, kConvThreads, 0, st>>>(a, (unsigned)blocks); break;
-    default: conv_bwd_kernel<Tin, 4><<<grid, kConvThreads, 0, st>>>(a, (unsigned)blocks); break;
+    case 2: return launch_ring(conv_bwd_kernel<Tin, 2>, a, blocks, empty, bytes, st);
+    case 3: return launch_ring(conv_bwd_kernel<Tin, 3>, a, blocks, empty, bytes, st);
+    default: return launch_ring(conv_bwd_kernel<Tin, 4>, a, blocks, empty, bytes, st);
   }
-  return cudaGetLastError();
 }
 
 // argument checks that the three entries share (after the null checks)
@@ -645,7 +719,7 @@ kda_status kda_short_conv_fwd(const void* x, int64_t x_stride, const float* weig
                        {workspace, (int64_t)kStatusBytes}};
   if (kda_status s = check_spans(ins, outs)) return s;
   if (workspace_bytes < kStatusBytes) return KDA_ERR_WORKSPACE;
-  const int V = kFV;
+  const int V = (int)(16 / es);
   ConvArgs a{};
   a.x = x;
   a.x_stride = x_stride;
@@ -660,7 +734,7 @@ kda_status kda_short_conv_fwd(const void* x, int64_t x_stride, const float* weig
   a.silu = activation == KDA_ACT_SILU;
   a.out = out;
   a.final_state = final_state;
-  a.strip = strip_len(total, D / V, kUnroll, 32, kWantThreads);
+  a.strip = strip_len(total, D / V, 8, 128);
   a.strips = (int)((total + a.strip - 1) / a.strip);
   a.sb = static_cast<StatusBlock*>(workspace);
   if (!grid_fits((int64_t)a.strips * (D / V)) || !grid_fits(N * (W - 1) * (D / V)))

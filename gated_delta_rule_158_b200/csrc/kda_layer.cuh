@@ -190,6 +190,87 @@ __device__ __forceinline__ float sigmoid_fast(float x) {
   return y;
 }
 
+// two fp32 values side by side, one instruction for both
+using f2 = unsigned long long;
+__device__ __forceinline__ f2 pack2(float a, float b) {
+  f2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ void unpack2(f2 v, float& a, float& b) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
+}
+__device__ __forceinline__ f2 fma2(f2 a, f2 b, f2 c) {
+  f2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ f2 mul2(f2 a, f2 b) {
+  f2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ f2 add2(f2 a, f2 b) {
+  f2 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ f2 ex2_2(f2 v) {
+  float a, b;
+  unpack2(v, a, b);
+  return pack2(ex2(a), ex2(b));
+}
+__device__ __forceinline__ float sum2(f2 v) {
+  float a, b;
+  unpack2(v, a, b);
+  return a + b;
+}
+__device__ __forceinline__ f2 zero2() { return 0ull; }
+
+// sigmoid_fast of both
+__device__ __forceinline__ f2 sigmoid2(f2 x) {
+  float a, b;
+  unpack2(add2(ex2_2(mul2(x, pack2(-kLog2e, -kLog2e))), pack2(1.f, 1.f)), a, b);
+  asm("rcp.approx.ftz.f32 %0, %0;" : "+f"(a));
+  asm("rcp.approx.ftz.f32 %0, %0;" : "+f"(b));
+  return pack2(a, b);
+}
+
+// ------------------------------------------------------- asynchronous copies
+// BYTES (4, 8, 16 or 32) from global to shared memory without registers; zeros
+// where !in (the source is not read then)
+template <int BYTES>
+__device__ __forceinline__ void copy_in(char* to, const void* from, bool in) {
+  constexpr int N = BYTES < 16 ? BYTES : 16;
+#pragma unroll
+  for (int i = 0; i < BYTES; i += N) {
+    const uint32_t dst = (uint32_t)__cvta_generic_to_shared(to + i);
+    const char* src = static_cast<const char*>(from) + i;
+    if constexpr (N == 16)
+      asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
+                   "r"(in ? 16 : 0)
+                   : "memory");
+    else
+      asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(dst), "l"(src), "n"(N),
+                   "r"(in ? N : 0)
+                   : "memory");
+  }
+}
+__device__ __forceinline__ void copies_issued() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+__device__ __forceinline__ void copies_landed() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+
+// all but the latest N committed groups of copies have landed
+template <int N>
+__device__ __forceinline__ void copies_landed_but() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// V elements of a slot as fp32
+template <typename T, int V>
+__device__ __forceinline__ void read_slot(const char* p, float (&v)[V]) {
+  load_vec<T, V>(reinterpret_cast<const T*>(p), v);
+}
+
 // -------------------------------------------------------------- raw values
 // V elements as they lie in memory, so that loads stay in flight until their
 // first use
@@ -216,6 +297,19 @@ struct Raw {
         const uint4 u = reinterpret_cast<const uint4*>(p)[i / 4];
         r[i] = u.x; r[i + 1] = u.y; r[i + 2] = u.z; r[i + 3] = u.w;
       }
+    }
+  }
+  __device__ __forceinline__ void store(T* p) const {
+    if constexpr (BYTES == 2) {
+      *reinterpret_cast<unsigned short*>(p) = (unsigned short)r[0];
+    } else if constexpr (BYTES == 4) {
+      *reinterpret_cast<uint32_t*>(p) = r[0];
+    } else if constexpr (BYTES == 8) {
+      *reinterpret_cast<uint2*>(p) = make_uint2(r[0], r[1]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < N; i += 4)
+        reinterpret_cast<uint4*>(p)[i / 4] = make_uint4(r[i], r[i + 1], r[i + 2], r[i + 3]);
     }
   }
   __device__ __forceinline__ void get(float (&v)[V]) const {

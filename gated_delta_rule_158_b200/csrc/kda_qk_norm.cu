@@ -6,13 +6,12 @@
 //
 // HBM-bound: every row is read once and written once (the gradients add one
 // fp32 row each way).  A row of d elements lies in a group of L lanes, 8
-// elements a lane, so the row's sum is log2 L shuffles and the rotation's
-// partner elements are in the same lane (pairs) or in one other lane of the
-// group (halves: rot_dim / 2 is a multiple of 8, so whole 8-element pieces
-// change places).  A block takes whole tokens, all their heads, so that the
-// angles' cosines and sines are formed once per token (fp64 product and
-// reduction to one turn, then fp32 sincospi) and read from shared memory by
-// all heads; the rows' loads are issued before they are formed.
+// elements a lane, so the row's sum is log2 L shuffles; a lane's elements are
+// chosen so that both of a turning pair are its own.  Blocks walk over tiles of
+// whole tokens, all their heads, so that an angle's cosine and sine are formed
+// once per token (fp64 product and reduction to one turn, then fp32 sincospi)
+// and read from shared memory by all heads, a tile ahead; the next rows are in
+// flight while a step's are worked on.
 #include <math.h>
 
 #include "kda_layer.cuh"
@@ -65,35 +64,83 @@ __device__ __forceinline__ void fill_turns(const NormArgs& a, int t0, int nt, fl
   }
 }
 
-// Turns the 8 elements v of lane l (elements 8 l ..) by the table row `tab`;
-// sgn = 1 forward, -1 back.  All lanes of the warp take part.
 enum Rot { kNoRot, kHalves, kPairs };
 
-template <int L, int ROT>
+// A lane's 8 elements of a row are two pieces of 4: neighbours, but with the
+// halves of the rotated part turning together, piece 0 from its first half and
+// piece 1 from the second, so that both elements of a pair are in the lane.
+struct Pieces {
+  int o0, o1;
+};
+template <int ROT>
+__device__ __forceinline__ Pieces pieces_of(const NormArgs& a, int l) {
+  Pieces p;
+  p.o0 = 8 * l;
+  p.o1 = 8 * l + 4;
+  if (ROT == kHalves && 8 * l < a.rot) {
+    p.o0 = 4 * l;
+    p.o1 = a.rot / 2 + 4 * l;
+  }
+  return p;
+}
+
+template <typename T, int ROT>
+struct RowRaw {  // 8 elements as they lie in memory
+  static constexpr int N = ROT == kHalves ? 2 : 1;
+  Raw<T, 8 / N> r[N];
+  __device__ __forceinline__ void zero() {
+#pragma unroll
+    for (int i = 0; i < N; ++i) r[i].zero();
+  }
+  __device__ __forceinline__ void load(const T* row, const Pieces& p) {
+    r[0].load(row + p.o0);
+    if constexpr (N == 2) r[1].load(row + p.o1);
+  }
+  __device__ __forceinline__ void get(float (&v)[8]) const {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = r[i / (8 / N)].at(i % (8 / N));
+  }
+};
+
+template <int ROT, typename T>
+__device__ __forceinline__ void store_row(T* row, const Pieces& p, const float (&v)[8]) {
+  if constexpr (ROT == kHalves) {
+    const float lo[4] = {v[0], v[1], v[2], v[3]}, hi[4] = {v[4], v[5], v[6], v[7]};
+    store_vec<4>(row + p.o0, lo);
+    store_vec<4>(row + p.o1, hi);
+  } else {
+    store_vec<8>(row + p.o0, v);
+  }
+}
+
+template <int ROT>
+__device__ __forceinline__ void load_weight(const float* w, const Pieces& p, float (&v)[8]) {
+  float lo[4], hi[4];
+  load_vec<float, 4>(w + p.o0, lo);
+  load_vec<float, 4>(w + p.o1, hi);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    v[i] = lo[i];
+    v[4 + i] = hi[i];
+  }
+}
+
+// Turns the lane's four pairs, numbers 4 l .. of the row, by the table row
+// `tab`; sgn = 1 forward, -1 back.
+template <int ROT>
 __device__ __forceinline__ void turn(const NormArgs& a, const float2* tab, int l, float sgn,
                                      float (&v)[8]) {
-  if constexpr (ROT == kPairs) {
-    if (8 * l < a.rot) {
+  if (ROT == kNoRot || 8 * l >= a.rot) return;
 #pragma unroll
-      for (int i = 0; i < 8; i += 2) {
-        const float2 cs = tab[4 * l + i / 2];
-        const float p = v[i], q = v[i + 1], s = sgn * cs.y;
-        v[i] = p * cs.x - q * s;
-        v[i + 1] = q * cs.x + p * s;
-      }
-    }
-  } else if constexpr (ROT == kHalves) {
-    const int hl = a.rot >> 4;  // lanes in half of the rotated part
-    const bool lo = l < hl, in = l < 2 * hl;
-    const int src = in ? (lo ? l + hl : l - hl) : l;
-    const float2* row = tab + 8 * (lo ? l : l - hl);
+  for (int i = 0; i < 4; i += 2) {
+    const float4 cs = *reinterpret_cast<const float4*>(tab + 4 * l + i);
+    const float c[2] = {cs.x, cs.z}, s[2] = {sgn * cs.y, sgn * cs.w};
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const float o = __shfl_sync(0xffffffffu, v[i], src, L);
-      if (in) {
-        const float2 cs = row[i];
-        v[i] = v[i] * cs.x + (lo ? -o : o) * (sgn * cs.y);
-      }
+    for (int k = 0; k < 2; ++k) {
+      const int p = ROT == kHalves ? i + k : 2 * (i + k), q = ROT == kHalves ? 4 + i + k : p + 1;
+      const float x = v[p], y = v[q];
+      v[p] = x * c[k] - y * s[k];
+      v[q] = y * c[k] + x * s[k];
     }
   }
 }
@@ -134,15 +181,16 @@ __device__ __forceinline__ int64_t dense_row(const NormArgs& a, int64_t t, const
 // or the next) are in flight while a step's are worked on.
 template <typename Tin, int L, int ROT>
 __global__ void __launch_bounds__(kNormThreads, 4) qk_norm_fwd_kernel(const NormArgs a) {
-  extern __shared__ float2 tab[];
+  extern __shared__ __align__(16) float2 tab[];
   constexpr int G = kNormThreads / L;  // lane groups
   constexpr int U = kRows<Tin>;
   const int l = threadIdx.x % L, grp = threadIdx.x / L;
   const bool act = 8 * l < a.d;
+  const Pieces pc = pieces_of<ROT>(a, l);
   const int H = a.Hq + a.Hk;
   const int steps = (a.per_block * H + G * U - 1) / (G * U);  // of a whole tile
   const int tiles = (int)(((int64_t)a.tokens + a.per_block - 1) / a.per_block);
-  Raw<Tin, 8> next[U];
+  RowRaw<Tin, ROT> next[U];
   auto fetch = [&](int tile, int s) {
     const int t0 = tile * a.per_block;
     const int rows = min(a.per_block, a.tokens - t0) * H;
@@ -152,21 +200,33 @@ __global__ void __launch_bounds__(kNormThreads, 4) qk_norm_fwd_kernel(const Norm
       next[u].zero();
       if (row < rows && act) {
         const Row r = row_of(a, row, H);
-        next[u].load(in_row<Tin>(a, t0 + r.tok, r) + 8 * l);
+        next[u].load(in_row<Tin>(a, t0 + r.tok, r), pc);
       }
     }
   };
-  if ((int)blockIdx.x < tiles) fetch(blockIdx.x, 0);
-  for (int tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
-    const int t0 = tile * a.per_block;
-    const int nt = min(a.per_block, a.tokens - t0), rows = nt * H;
+  if ((int)blockIdx.x < tiles) {
+    fetch(blockIdx.x, 0);
     if (ROT != kNoRot) {
-      if (tile != (int)blockIdx.x) __syncthreads();  // the last tile's table has been read
-      fill_turns(a, t0, nt, tab);
+      const int t0 = blockIdx.x * a.per_block;
+      fill_turns(a, t0, min(a.per_block, a.tokens - t0), tab);
+    }
+  }
+  for (int tile = blockIdx.x, k = 0; tile < tiles; tile += gridDim.x, ++k) {
+    const int t0 = tile * a.per_block;
+    const int rows = min(a.per_block, a.tokens - t0) * H;
+    const float2* tb = tab;
+    if (ROT != kNoRot) {
+      // the table of the tile after this one is formed while this is worked on:
+      // two tables, one barrier per tile
+      tb = tab + (k & 1) * a.per_block * (a.rot >> 1);
       __syncthreads();
+      const int64_t t2 = ((int64_t)tile + gridDim.x) * a.per_block;
+      if (t2 < a.tokens)
+        fill_turns(a, (int)t2, (int)min((int64_t)a.per_block, a.tokens - t2),
+                   tab + (~k & 1) * a.per_block * (a.rot >> 1));
     }
     for (int s = 0; s < steps; ++s) {
-      Raw<Tin, 8> cur[U];
+      RowRaw<Tin, ROT> cur[U];
 #pragma unroll
       for (int u = 0; u < U; ++u) cur[u] = next[u];
       if (s + 1 < steps) fetch(tile, s + 1);
@@ -183,7 +243,7 @@ __global__ void __launch_bounds__(kNormThreads, 4) qk_norm_fwd_kernel(const Norm
         const float* wp = r.isq ? a.q_weight : a.k_weight;
         if (wp && act) {
           float w[8];
-          load_vec<float, 8>(wp + 8 * l, w);
+          load_weight<ROT>(wp, pc, w);
 #pragma unroll
           for (int i = 0; i < 8; ++i) x[i] *= f * w[i];
         } else {
@@ -192,10 +252,10 @@ __global__ void __launch_bounds__(kNormThreads, 4) qk_norm_fwd_kernel(const Norm
         }
         // rows past the end turn by the table's first token; nothing is stored
         if (ROT != kNoRot)
-          turn<L, ROT>(a, tab + (row < rows ? r.tok : 0) * (a.rot >> 1), l, 1.f, x);
+          turn<ROT>(a, tb + (row < rows ? r.tok : 0) * (a.rot >> 1), l, 1.f, x);
         if (row < rows && act)
-          store_vec<8>(static_cast<Tin*>(r.isq ? a.q_out : a.k_out) +
-                           dense_row(a, t0 + r.tok, r) + 8 * l, x);
+          store_row<ROT>(static_cast<Tin*>(r.isq ? a.q_out : a.k_out) +
+                             dense_row(a, t0 + r.tok, r), pc, x);
       }
     }
   }
@@ -206,19 +266,20 @@ __global__ void __launch_bounds__(kNormThreads, 4) qk_norm_fwd_kernel(const Norm
 // block's groups in order, and leaves as one partial row per block.
 template <typename Tin, int L, int ROT>
 __global__ void __launch_bounds__(kNormThreads, 2) qk_norm_bwd_kernel(const NormArgs a) {
-  extern __shared__ float2 tab[];
+  extern __shared__ __align__(16) float2 tab[];
   constexpr int G = kNormThreads / L;
   constexpr int U = 2;
   const int l = threadIdx.x % L, grp = threadIdx.x / L;
   const bool act = 8 * l < a.d;
+  const Pieces pc = pieces_of<ROT>(a, l);
   const int H = a.Hq + a.Hk;
   const int steps = (a.per_block * H + G * U - 1) / (G * U);  // of a whole tile
   const int tiles = (int)(((int64_t)a.tokens + a.per_block - 1) / a.per_block);
   float gq[8], gk[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) gq[i] = gk[i] = 0.f;
-  Raw<Tin, 8> nx[U];
-  Raw<float, 8> nd[U];
+  RowRaw<Tin, ROT> nx[U];
+  RowRaw<float, ROT> nd[U];
   auto fetch = [&](int tile, int s) {
     const int t0 = tile * a.per_block;
     const int rows = min(a.per_block, a.tokens - t0) * H;
@@ -229,23 +290,35 @@ __global__ void __launch_bounds__(kNormThreads, 2) qk_norm_bwd_kernel(const Norm
       nd[u].zero();
       if (row < rows && act) {
         const Row r = row_of(a, row, H);
-        nx[u].load(in_row<Tin>(a, t0 + r.tok, r) + 8 * l);
-        nd[u].load((r.isq ? a.dq_out : a.dk_out) + dense_row(a, t0 + r.tok, r) + 8 * l);
+        nx[u].load(in_row<Tin>(a, t0 + r.tok, r), pc);
+        nd[u].load((r.isq ? a.dq_out : a.dk_out) + dense_row(a, t0 + r.tok, r), pc);
       }
     }
   };
-  if ((int)blockIdx.x < tiles) fetch(blockIdx.x, 0);
-  for (int tile = blockIdx.x; tile < tiles; tile += a.blocks) {
-    const int t0 = tile * a.per_block;
-    const int nt = min(a.per_block, a.tokens - t0), rows = nt * H;
+  if ((int)blockIdx.x < tiles) {
+    fetch(blockIdx.x, 0);
     if (ROT != kNoRot) {
-      if (tile != (int)blockIdx.x) __syncthreads();  // the last tile's table has been read
-      fill_turns(a, t0, nt, tab);
+      const int t0 = blockIdx.x * a.per_block;
+      fill_turns(a, t0, min(a.per_block, a.tokens - t0), tab);
+    }
+  }
+  for (int tile = blockIdx.x, k = 0; tile < tiles; tile += a.blocks, ++k) {
+    const int t0 = tile * a.per_block;
+    const int rows = min(a.per_block, a.tokens - t0) * H;
+    const float2* tb = tab;
+    if (ROT != kNoRot) {
+      // the table of the tile after this one is formed while this is worked on:
+      // two tables, one barrier per tile
+      tb = tab + (k & 1) * a.per_block * (a.rot >> 1);
       __syncthreads();
+      const int64_t t2 = ((int64_t)tile + a.blocks) * a.per_block;
+      if (t2 < a.tokens)
+        fill_turns(a, (int)t2, (int)min((int64_t)a.per_block, a.tokens - t2),
+                   tab + (~k & 1) * a.per_block * (a.rot >> 1));
     }
     for (int s = 0; s < steps; ++s) {
-      Raw<Tin, 8> cx[U];
-      Raw<float, 8> cd[U];
+      RowRaw<Tin, ROT> cx[U];
+      RowRaw<float, ROT> cd[U];
 #pragma unroll
       for (int u = 0; u < U; ++u) {
         cx[u] = nx[u];
@@ -264,7 +337,7 @@ __global__ void __launch_bounds__(kNormThreads, 2) qk_norm_bwd_kernel(const Norm
         for (int i = 0; i < 8; ++i) ss = fmaf(x[i], x[i], ss);
         const float f = rsqrtf(fmaf(a.c, group_sum<L>(ss), a.eps));
         if (ROT != kNoRot)
-          turn<L, ROT>(a, tab + (row < rows ? r.tok : 0) * (a.rot >> 1), l, -1.f, dy);
+          turn<ROT>(a, tb + (row < rows ? r.tok : 0) * (a.rot >> 1), l, -1.f, dy);
 #pragma unroll
         for (int i = 0; i < 8; ++i) x[i] *= f;
         if (a.partial) {  // rows past the end are zero
@@ -279,7 +352,7 @@ __global__ void __launch_bounds__(kNormThreads, 2) qk_norm_bwd_kernel(const Norm
         const float* wp = r.isq ? a.q_weight : a.k_weight;
         if (wp && act) {
           float w[8];
-          load_vec<float, 8>(wp + 8 * l, w);
+          load_weight<ROT>(wp, pc, w);
 #pragma unroll
           for (int i = 0; i < 8; ++i) dy[i] *= w[i];
         }
@@ -290,7 +363,7 @@ __global__ void __launch_bounds__(kNormThreads, 2) qk_norm_bwd_kernel(const Norm
 #pragma unroll
         for (int i = 0; i < 8; ++i) dy[i] = f * fmaf(-x[i], m, dy[i]);
         if (row < rows && act)
-          store_vec<8>((r.isq ? a.dq : a.dk) + dense_row(a, t0 + r.tok, r) + 8 * l, dy);
+          store_row<ROT>((r.isq ? a.dq : a.dk) + dense_row(a, t0 + r.tok, r), pc, dy);
       }
     }
   }
@@ -300,8 +373,9 @@ __global__ void __launch_bounds__(kNormThreads, 2) qk_norm_bwd_kernel(const Norm
   __syncthreads();
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    red[(grp * 2 + 0) * 8 * L + 8 * l + i] = gq[i];
-    red[(grp * 2 + 1) * 8 * L + 8 * l + i] = gk[i];
+    const int col = i < 4 ? pc.o0 + i : pc.o1 + i - 4;
+    red[(grp * 2 + 0) * 8 * L + col] = gq[i];
+    red[(grp * 2 + 1) * 8 * L + col] = gk[i];
   }
   __syncthreads();
   for (int e = threadIdx.x; e < 2 * 8 * L; e += kNormThreads) {
@@ -336,15 +410,14 @@ __global__ void __launch_bounds__(256) qk_norm_bwd_sum_kernel(const float* __res
 int lane_group(int d) { return d <= 32 ? 4 : d <= 64 ? 8 : d <= 128 ? 16 : 32; }
 
 // Tokens per tile: enough rows for kRowsInFlight per lane group; with a
-// rotation more, so that the block's threads form the angles of several tokens
-// at once (a token's 32 to 128 angles alone leave most of them waiting), as
-// long as every SM has four blocks.
+// rotation up to four times as many, so that more of the block's threads form
+// angles, while every SM has a few tiles.
 int tokens_per_block(int tokens, int H, int d, int rot) {
   const int groups = kNormThreads / lane_group(d);
   int n = groups * kRowsInFlight / H;
   if (rot > 0) {
-    int m = 2 * kNormThreads / rot;
-    if (m > tokens / (148 * 4)) m = tokens / (148 * 4);
+    int m = 4;
+    if (m > tokens / (148 * 8)) m = tokens / (148 * 8);
     if (n < m) n = m;
   }
   if (n > kMaxTokens) n = kMaxTokens;
@@ -357,7 +430,7 @@ int bwd_blocks(int tokens, int per_block) {
   return (int)(n < kBwdBlocks ? n : kBwdBlocks);
 }
 
-size_t table_bytes(const NormArgs& a) { return sizeof(float2) * (size_t)a.per_block * (a.rot / 2); }
+size_t table_bytes(const NormArgs& a) { return 2 * sizeof(float2) * (size_t)a.per_block * (a.rot / 2); }
 
 template <typename Tin, int ROT>
 cudaError_t dispatch_fwd_rot(const NormArgs& a, cudaStream_t st) {

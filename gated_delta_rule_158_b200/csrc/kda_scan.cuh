@@ -116,44 +116,6 @@ __device__ __forceinline__ Channels channels_of(const Args& a, int cb) {
 }
 inline int channel_blocks(int D, int G, int CT) { return G * ((D / G + CT - 1) / CT); }
 
-// ------------------------------------------------------------- arithmetic
-// two fp32 values side by side, one instruction for both
-using f2 = unsigned long long;
-__device__ __forceinline__ f2 pack2(float a, float b) {
-  f2 r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
-  return r;
-}
-__device__ __forceinline__ void unpack2(f2 v, float& a, float& b) {
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
-}
-__device__ __forceinline__ f2 fma2(f2 a, f2 b, f2 c) {
-  f2 r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-  return r;
-}
-__device__ __forceinline__ f2 mul2(f2 a, f2 b) {
-  f2 r;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-__device__ __forceinline__ f2 add2(f2 a, f2 b) {
-  f2 r;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-__device__ __forceinline__ f2 ex2_2(f2 v) {
-  float a, b;
-  unpack2(v, a, b);
-  return pack2(ex2(a), ex2(b));
-}
-__device__ __forceinline__ float sum2(f2 v) {
-  float a, b;
-  unpack2(v, a, b);
-  return a + b;
-}
-__device__ __forceinline__ f2 zero2() { return 0ull; }
-
 // 2 N consecutive floats as N pairs (aligned to their size)
 template <int N>
 __device__ __forceinline__ void load_pairs(const float* p, f2 (&v)[N]) {
@@ -201,35 +163,6 @@ __device__ __forceinline__ void step_sizes(float (&v)[V], bool softplus) {
     v[j] = fmaxf(v[j], 0.f) + p;
     if (V > 1) v[V > 1 ? j + 1 : 0] = fmaxf(b, 0.f) + q;
   }
-}
-
-// ------------------------------------------------------- asynchronous copies
-// BYTES (4, 8, 16 or 32) from global to shared memory without registers; zeros
-// where !in (the source is not read then)
-template <int BYTES>
-__device__ __forceinline__ void copy_in(char* to, const void* from, bool in) {
-  constexpr int N = BYTES < 16 ? BYTES : 16;
-#pragma unroll
-  for (int i = 0; i < BYTES; i += N) {
-    const uint32_t dst = (uint32_t)__cvta_generic_to_shared(to + i);
-    const char* src = static_cast<const char*>(from) + i;
-    if constexpr (N == 16)
-      asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
-                   "r"(in ? 16 : 0)
-                   : "memory");
-    else
-      asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(dst), "l"(src), "n"(N),
-                   "r"(in ? N : 0)
-                   : "memory");
-  }
-}
-__device__ __forceinline__ void copies_issued() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-__device__ __forceinline__ void copies_landed() { asm volatile("cp.async.wait_all;" ::: "memory"); }
-
-// V elements of a slot as fp32
-template <typename T, int V>
-__device__ __forceinline__ void read_slot(const char* p, float (&v)[V]) {
-  load_vec<T, V>(reinterpret_cast<const T*>(p), v);
 }
 
 // Sums of four tokens' values over the LN lanes of a channel.  LN >= 4: lane
