@@ -227,6 +227,23 @@ __device__ __forceinline__ float sum2(f2 v) {
 }
 __device__ __forceinline__ f2 zero2() { return 0ull; }
 
+// 2 N consecutive floats as N pairs (aligned to their size)
+template <int N>
+__device__ __forceinline__ void load_pairs(const float* p, f2 (&v)[N]) {
+  if constexpr (N == 1) {
+    v[0] = *reinterpret_cast<const f2*>(p);
+  } else {
+    const ulonglong2 u = *reinterpret_cast<const ulonglong2*>(p);
+    v[0] = u.x;
+    v[1] = u.y;
+  }
+}
+template <int N>
+__device__ __forceinline__ void store_pairs(float* p, const f2 (&v)[N]) {
+  if constexpr (N == 1) *reinterpret_cast<f2*>(p) = v[0];
+  else *reinterpret_cast<ulonglong2*>(p) = make_ulonglong2(v[0], v[1]);
+}
+
 // sigmoid_fast of both
 __device__ __forceinline__ f2 sigmoid2(f2 x) {
   float a, b;

@@ -20,11 +20,12 @@ namespace kda {
 namespace {
 
 constexpr int kNormThreads = 256;
-// rows per lane group and step: 64 bytes in flight a lane
+// rows per lane group and step, and as many in flight: 64 bytes a lane, 96 with
+// the gradients' fp32 cotangent beside bf16 rows
 template <typename Tin>
 constexpr int kRows = 8 / (int)sizeof(Tin);
-constexpr int kRowsInFlight = 4;
-constexpr int kMaxTokens = 16;    // tokens per block (shared table: 16 x 256 floats)
+constexpr int kBwdRows = 2;
+constexpr int kMaxTokens = 16;  // tokens per tile (two shared tables: 2 x 16 x 256 floats)
 
 struct NormArgs {
   const void* q;
@@ -39,7 +40,8 @@ struct NormArgs {
   bool pairs;
   void* q_out;
   void* k_out;
-  int per_block;  // tokens per block
+  int per_block;  // tokens per tile
+  int hs, ts;     // heads x tokens of a block's lane groups
   int blocks;
   // gradients
   const float* dq_out;
@@ -49,8 +51,9 @@ struct NormArgs {
   float* partial;  // [blocks][2][d]
 };
 
-// cos and sin of positions[t0 + i] * inv_freq[j] for the block's tokens
-__device__ __forceinline__ void fill_turns(const NormArgs& a, int t0, int nt, float2* tab) {
+// cos and sin of positions[t0 + i] * inv_freq[j] for the tile's tokens: a token's
+// cosines, then its sines
+__device__ __forceinline__ void fill_turns(const NormArgs& a, int t0, int nt, float* tab) {
   const int half = a.rot >> 1;
   for (int e = threadIdx.x; e < nt * half; e += kNormThreads) {
     const int i = e / half, j = e - i * half;
@@ -60,7 +63,8 @@ __device__ __forceinline__ void fill_turns(const NormArgs& a, int t0, int nt, fl
     const double f = x - 2.0 * rint(0.5 * x);
     float s, co;
     sincospif((float)f, &s, &co);
-    tab[e] = make_float2(co, s);
+    tab[i * a.rot + j] = co;
+    tab[i * a.rot + half + j] = s;
   }
 }
 
@@ -125,22 +129,33 @@ __device__ __forceinline__ void load_weight(const float* w, const Pieces& p, flo
   }
 }
 
-// Turns the lane's four pairs, numbers 4 l .. of the row, by the table row
-// `tab`; sgn = 1 forward, -1 back.
+// Turns the lane's four pairs, numbers 4 l .. of the row, by the angles of the
+// tile's token tok; sgn = 1 forward, -1 back.
 template <int ROT>
-__device__ __forceinline__ void turn(const NormArgs& a, const float2* tab, int l, float sgn,
-                                     float (&v)[8]) {
+__device__ __forceinline__ void turn(const NormArgs& a, const float* tab, int tok, int l,
+                                     float sgn, float (&v)[8]) {
   if (ROT == kNoRot || 8 * l >= a.rot) return;
+  const float* at = tab + tok * a.rot + 4 * l;
+  if constexpr (ROT == kHalves) {
+    f2 c[2], s[2];
+    load_pairs<2>(at, c);
+    load_pairs<2>(at + (a.rot >> 1), s);
+    const f2 one = pack2(sgn, sgn), neg = pack2(-sgn, -sgn);
 #pragma unroll
-  for (int i = 0; i < 4; i += 2) {
-    const float4 cs = *reinterpret_cast<const float4*>(tab + 4 * l + i);
-    const float c[2] = {cs.x, cs.z}, s[2] = {sgn * cs.y, sgn * cs.w};
+    for (int i = 0; i < 2; ++i) {
+      const f2 p = pack2(v[2 * i], v[2 * i + 1]), q = pack2(v[4 + 2 * i], v[5 + 2 * i]);
+      unpack2(fma2(p, c[i], mul2(q, mul2(s[i], neg))), v[2 * i], v[2 * i + 1]);
+      unpack2(fma2(q, c[i], mul2(p, mul2(s[i], one))), v[4 + 2 * i], v[5 + 2 * i]);
+    }
+  } else {
+    float c[4], s[4];
+    load_vec<float, 4>(at, c);
+    load_vec<float, 4>(at + (a.rot >> 1), s);
 #pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      const int p = ROT == kHalves ? i + k : 2 * (i + k), q = ROT == kHalves ? 4 + i + k : p + 1;
-      const float x = v[p], y = v[q];
-      v[p] = x * c[k] - y * s[k];
-      v[q] = y * c[k] + x * s[k];
+    for (int i = 0; i < 4; ++i) {
+      const float p = v[2 * i], q = v[2 * i + 1], sn = sgn * s[i];
+      v[2 * i] = p * c[i] - q * sn;
+      v[2 * i + 1] = q * c[i] + p * sn;
     }
   }
 }
@@ -152,171 +167,166 @@ __device__ __forceinline__ float group_sum(float s) {
   return s;
 }
 
-// A row of the block's tile: its token and where it lies.
-struct Row {
-  int tok, head;  // head of q, or of k from Hq on
+// A block's lane groups stand for HS heads x TS tokens of its tile; a group
+// takes every HS-th head and, of a head, U tokens TS apart at a time.  What
+// depends on the head (its tensor, row length, weight) is chosen once per head.
+template <typename Tin>
+struct Head {
+  const Tin* in;       // the group's first row of the tile
+  int64_t step;        // to its next
   bool isq;
 };
 
-__device__ __forceinline__ Row row_of(const NormArgs& a, int row, int H) {
-  Row r;
-  r.tok = a.per_block == 1 ? 0 : row / H;
-  r.head = row - r.tok * H;
-  r.isq = r.head < a.Hq;
+template <typename Tin>
+__device__ __forceinline__ Head<Tin> head_of(const NormArgs& a, int h, int64_t t) {
+  Head<Tin> r;
+  r.isq = h < a.Hq;
+  const int64_t stride = r.isq ? a.q_stride : a.k_stride;
+  r.in = static_cast<const Tin*>(r.isq ? a.q : a.k) + (r.isq ? h : h - a.Hq) * a.d + t * stride;
+  r.step = a.ts * stride;
   return r;
 }
 
-template <typename Tin>
-__device__ __forceinline__ const Tin* in_row(const NormArgs& a, int64_t t, const Row& r) {
-  return r.isq ? static_cast<const Tin*>(a.q) + t * a.q_stride + r.head * a.d
-               : static_cast<const Tin*>(a.k) + t * a.k_stride + (r.head - a.Hq) * a.d;
+// the same of a dense q- or k-shaped tensor
+__device__ __forceinline__ int64_t dense_row(const NormArgs& a, int h, int64_t t) {
+  return h < a.Hq ? (t * a.Hq + h) * a.d : (t * a.Hk + h - a.Hq) * a.d;
+}
+__device__ __forceinline__ int64_t dense_step(const NormArgs& a, int h) {
+  return (int64_t)a.ts * (h < a.Hq ? a.Hq : a.Hk) * a.d;
 }
 
-// offset of a row of a dense q- or k-shaped tensor
-__device__ __forceinline__ int64_t dense_row(const NormArgs& a, int64_t t, const Row& r) {
-  return r.isq ? (t * a.Hq + r.head) * a.d : (t * a.Hk + r.head - a.Hq) * a.d;
-}
-
-// Blocks walk over tiles of per_block tokens; the next step's rows (of this tile
-// or the next) are in flight while a step's are worked on.
+// Blocks walk over tiles of per_block <= U TS tokens; the next head's rows (of
+// this tile or the next) are in flight while a head's are worked on.
 template <typename Tin, int L, int ROT>
 __global__ void __launch_bounds__(kNormThreads, 4) qk_norm_fwd_kernel(const NormArgs a) {
-  extern __shared__ __align__(16) float2 tab[];
-  constexpr int G = kNormThreads / L;  // lane groups
+  extern __shared__ __align__(16) float tab[];
   constexpr int U = kRows<Tin>;
   const int l = threadIdx.x % L, grp = threadIdx.x / L;
-  const bool act = 8 * l < a.d;
+  const int hs = grp % a.hs, ts = grp / a.hs;
+  const bool act = 8 * l < a.d && ts < a.ts;
   const Pieces pc = pieces_of<ROT>(a, l);
   const int H = a.Hq + a.Hk;
-  const int steps = (a.per_block * H + G * U - 1) / (G * U);  // of a whole tile
   const int tiles = (int)(((int64_t)a.tokens + a.per_block - 1) / a.per_block);
   RowRaw<Tin, ROT> next[U];
-  auto fetch = [&](int tile, int s) {
-    const int t0 = tile * a.per_block;
-    const int rows = min(a.per_block, a.tokens - t0) * H;
+  auto fetch = [&](int tile, int h) {
+    const int t0 = tile * a.per_block, nt = min(a.per_block, a.tokens - t0);
+    const Head<Tin> r = head_of<Tin>(a, h, t0 + ts);
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const int row = (s * U + u) * G + grp;
       next[u].zero();
-      if (row < rows && act) {
-        const Row r = row_of(a, row, H);
-        next[u].load(in_row<Tin>(a, t0 + r.tok, r), pc);
-      }
+      if (act && h < H && ts + u * a.ts < nt) next[u].load(r.in + u * r.step, pc);
     }
   };
   if ((int)blockIdx.x < tiles) {
-    fetch(blockIdx.x, 0);
+    fetch(blockIdx.x, hs);
     if (ROT != kNoRot) {
       const int t0 = blockIdx.x * a.per_block;
       fill_turns(a, t0, min(a.per_block, a.tokens - t0), tab);
     }
   }
   for (int tile = blockIdx.x, k = 0; tile < tiles; tile += gridDim.x, ++k) {
-    const int t0 = tile * a.per_block;
-    const int rows = min(a.per_block, a.tokens - t0) * H;
-    const float2* tb = tab;
+    const int t0 = tile * a.per_block, nt = min(a.per_block, a.tokens - t0);
+    const float* tb = tab;
     if (ROT != kNoRot) {
       // the table of the tile after this one is formed while this is worked on:
       // two tables, one barrier per tile
-      tb = tab + (k & 1) * a.per_block * (a.rot >> 1);
+      tb = tab + (k & 1) * a.per_block * a.rot;
       __syncthreads();
       const int64_t t2 = ((int64_t)tile + gridDim.x) * a.per_block;
       if (t2 < a.tokens)
         fill_turns(a, (int)t2, (int)min((int64_t)a.per_block, a.tokens - t2),
-                   tab + (~k & 1) * a.per_block * (a.rot >> 1));
+                   tab + (~k & 1) * a.per_block * a.rot);
     }
-    for (int s = 0; s < steps; ++s) {
+    for (int h0 = 0; h0 < H; h0 += a.hs) {
+      const int h = h0 + hs;
       RowRaw<Tin, ROT> cur[U];
 #pragma unroll
       for (int u = 0; u < U; ++u) cur[u] = next[u];
-      if (s + 1 < steps) fetch(tile, s + 1);
-      else if (tile + (int)gridDim.x < tiles) fetch(tile + gridDim.x, 0);
+      if (h0 + a.hs < H) fetch(tile, h + a.hs);
+      else if (tile + (int)gridDim.x < tiles) fetch(tile + gridDim.x, hs);
+      const bool isq = h < a.Hq;
+      Tin* out = static_cast<Tin*>(isq ? a.q_out : a.k_out) + dense_row(a, h, t0 + ts);
+      const int64_t step = dense_step(a, h);
+      const float* wp = isq ? a.q_weight : a.k_weight;
 #pragma unroll
       for (int u = 0; u < U; ++u) {
-        const int row = (s * U + u) * G + grp;
-        const Row r = row_of(a, row, H);
+        const int t = ts + u * a.ts;
         float x[8], ss = 0.f;
         cur[u].get(x);
 #pragma unroll
         for (int i = 0; i < 8; ++i) ss = fmaf(x[i], x[i], ss);
         const float f = rsqrtf(fmaf(a.c, group_sum<L>(ss), a.eps));
-        const float* wp = r.isq ? a.q_weight : a.k_weight;
-        if (wp && act) {
-          float w[8];
-          load_weight<ROT>(wp, pc, w);
 #pragma unroll
-          for (int i = 0; i < 8; ++i) x[i] *= f * w[i];
-        } else {
+        for (int i = 0; i < 8; ++i) x[i] *= f;
+        if (act && h < H && t < nt) {
+          if (wp) {
+            float w[8];
+            load_weight<ROT>(wp, pc, w);
 #pragma unroll
-          for (int i = 0; i < 8; ++i) x[i] *= f;
+            for (int i = 0; i < 8; ++i) x[i] *= w[i];
+          }
+          turn<ROT>(a, tb, t, l, 1.f, x);
+          store_row<ROT>(out + u * step, pc, x);
         }
-        // rows past the end turn by the table's first token; nothing is stored
-        if (ROT != kNoRot)
-          turn<ROT>(a, tb + (row < rows ? r.tok : 0) * (a.rot >> 1), l, 1.f, x);
-        if (row < rows && act)
-          store_row<ROT>(static_cast<Tin*>(r.isq ? a.q_out : a.k_out) +
-                             dense_row(a, t0 + r.tok, r), pc, x);
       }
     }
   }
 }
 
-// Blocks walk over token tiles; a lane's share of dweight (its 8 columns, the
-// rows of its group) stays in registers over the walk, is added over the
-// block's groups in order, and leaves as one partial row per block.
+// A lane's share of dweight (its 8 columns, the rows of its group) stays in
+// registers over the walk, is added over the block's groups in order, and
+// leaves as one partial row per block.
 template <typename Tin, int L, int ROT>
 __global__ void __launch_bounds__(kNormThreads, 2) qk_norm_bwd_kernel(const NormArgs a) {
-  extern __shared__ __align__(16) float2 tab[];
+  extern __shared__ __align__(16) float tab[];
   constexpr int G = kNormThreads / L;
-  constexpr int U = 2;
+  constexpr int U = kBwdRows;
   const int l = threadIdx.x % L, grp = threadIdx.x / L;
-  const bool act = 8 * l < a.d;
+  const int hs = grp % a.hs, ts = grp / a.hs;
+  const bool act = 8 * l < a.d && ts < a.ts;
   const Pieces pc = pieces_of<ROT>(a, l);
   const int H = a.Hq + a.Hk;
-  const int steps = (a.per_block * H + G * U - 1) / (G * U);  // of a whole tile
   const int tiles = (int)(((int64_t)a.tokens + a.per_block - 1) / a.per_block);
   float gq[8], gk[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) gq[i] = gk[i] = 0.f;
   RowRaw<Tin, ROT> nx[U];
   RowRaw<float, ROT> nd[U];
-  auto fetch = [&](int tile, int s) {
-    const int t0 = tile * a.per_block;
-    const int rows = min(a.per_block, a.tokens - t0) * H;
+  auto fetch = [&](int tile, int h) {
+    const int t0 = tile * a.per_block, nt = min(a.per_block, a.tokens - t0);
+    const Head<Tin> r = head_of<Tin>(a, h, t0 + ts);
+    const float* dy = (r.isq ? a.dq_out : a.dk_out) + dense_row(a, h, t0 + ts);
+    const int64_t step = dense_step(a, h);
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const int row = (s * U + u) * G + grp;
       nx[u].zero();
       nd[u].zero();
-      if (row < rows && act) {
-        const Row r = row_of(a, row, H);
-        nx[u].load(in_row<Tin>(a, t0 + r.tok, r), pc);
-        nd[u].load((r.isq ? a.dq_out : a.dk_out) + dense_row(a, t0 + r.tok, r), pc);
+      if (act && h < H && ts + u * a.ts < nt) {
+        nx[u].load(r.in + u * r.step, pc);
+        nd[u].load(dy + u * step, pc);
       }
     }
   };
   if ((int)blockIdx.x < tiles) {
-    fetch(blockIdx.x, 0);
+    fetch(blockIdx.x, hs);
     if (ROT != kNoRot) {
       const int t0 = blockIdx.x * a.per_block;
       fill_turns(a, t0, min(a.per_block, a.tokens - t0), tab);
     }
   }
   for (int tile = blockIdx.x, k = 0; tile < tiles; tile += a.blocks, ++k) {
-    const int t0 = tile * a.per_block;
-    const int rows = min(a.per_block, a.tokens - t0) * H;
-    const float2* tb = tab;
+    const int t0 = tile * a.per_block, nt = min(a.per_block, a.tokens - t0);
+    const float* tb = tab;
     if (ROT != kNoRot) {
-      // the table of the tile after this one is formed while this is worked on:
-      // two tables, one barrier per tile
-      tb = tab + (k & 1) * a.per_block * (a.rot >> 1);
+      tb = tab + (k & 1) * a.per_block * a.rot;
       __syncthreads();
       const int64_t t2 = ((int64_t)tile + a.blocks) * a.per_block;
       if (t2 < a.tokens)
         fill_turns(a, (int)t2, (int)min((int64_t)a.per_block, a.tokens - t2),
-                   tab + (~k & 1) * a.per_block * (a.rot >> 1));
+                   tab + (~k & 1) * a.per_block * a.rot);
     }
-    for (int s = 0; s < steps; ++s) {
+    for (int h0 = 0; h0 < H; h0 += a.hs) {
+      const int h = h0 + hs;
       RowRaw<Tin, ROT> cx[U];
       RowRaw<float, ROT> cd[U];
 #pragma unroll
@@ -324,24 +334,31 @@ __global__ void __launch_bounds__(kNormThreads, 2) qk_norm_bwd_kernel(const Norm
         cx[u] = nx[u];
         cd[u] = nd[u];
       }
-      if (s + 1 < steps) fetch(tile, s + 1);
-      else if (tile + a.blocks < tiles) fetch(tile + a.blocks, 0);
+      if (h0 + a.hs < H) fetch(tile, h + a.hs);
+      else if (tile + a.blocks < tiles) fetch(tile + a.blocks, hs);
+      const bool isq = h < a.Hq;
+      float* out = (isq ? a.dq : a.dk) + dense_row(a, h, t0 + ts);
+      const int64_t step = dense_step(a, h);
+      const float* wp = isq ? a.q_weight : a.k_weight;
+      float w[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) w[i] = 1.f;
+      if (wp && act) load_weight<ROT>(wp, pc, w);
 #pragma unroll
       for (int u = 0; u < U; ++u) {
-        const int row = (s * U + u) * G + grp;
-        const Row r = row_of(a, row, H);
+        const int t = ts + u * a.ts;
+        const bool in = act && h < H && t < nt;
         float x[8], dy[8], ss = 0.f;
         cx[u].get(x);
         cd[u].get(dy);
 #pragma unroll
         for (int i = 0; i < 8; ++i) ss = fmaf(x[i], x[i], ss);
         const float f = rsqrtf(fmaf(a.c, group_sum<L>(ss), a.eps));
-        if (ROT != kNoRot)
-          turn<ROT>(a, tb + (row < rows ? r.tok : 0) * (a.rot >> 1), l, -1.f, dy);
+        if (in) turn<ROT>(a, tb, t, l, -1.f, dy);
 #pragma unroll
         for (int i = 0; i < 8; ++i) x[i] *= f;
         if (a.partial) {  // rows past the end are zero
-          if (r.isq) {
+          if (isq) {
 #pragma unroll
             for (int i = 0; i < 8; ++i) gq[i] = fmaf(dy[i], x[i], gq[i]);
           } else {
@@ -349,27 +366,22 @@ __global__ void __launch_bounds__(kNormThreads, 2) qk_norm_bwd_kernel(const Norm
             for (int i = 0; i < 8; ++i) gk[i] = fmaf(dy[i], x[i], gk[i]);
           }
         }
-        const float* wp = r.isq ? a.q_weight : a.k_weight;
-        if (wp && act) {
-          float w[8];
-          load_weight<ROT>(wp, pc, w);
-#pragma unroll
-          for (int i = 0; i < 8; ++i) dy[i] *= w[i];
-        }
         float m = 0.f;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) m = fmaf(dy[i], x[i], m);
+        for (int i = 0; i < 8; ++i) {
+          dy[i] *= w[i];
+          m = fmaf(dy[i], x[i], m);
+        }
         m = a.c * group_sum<L>(m);
 #pragma unroll
         for (int i = 0; i < 8; ++i) dy[i] = f * fmaf(-x[i], m, dy[i]);
-        if (row < rows && act)
-          store_row<ROT>((r.isq ? a.dq : a.dk) + dense_row(a, t0 + r.tok, r), pc, dy);
+        if (in) store_row<ROT>(out + u * step, pc, dy);
       }
     }
   }
   if (!a.partial) return;
   // [group][2][8 L] over the shared memory of the table
-  float* red = reinterpret_cast<float*>(tab);
+  float* red = tab;
   __syncthreads();
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
@@ -409,28 +421,36 @@ __global__ void __launch_bounds__(256) qk_norm_bwd_sum_kernel(const float* __res
 
 int lane_group(int d) { return d <= 32 ? 4 : d <= 64 ? 8 : d <= 128 ? 16 : 32; }
 
-// Tokens per tile: enough rows for kRowsInFlight per lane group; with a
-// rotation up to four times as many, so that more of the block's threads form
-// angles, while every SM has a few tiles.
-int tokens_per_block(int tokens, int H, int d, int rot) {
-  const int groups = kNormThreads / lane_group(d);
-  int n = groups * kRowsInFlight / H;
-  if (rot > 0) {
-    int m = 4;
-    if (m > tokens / (148 * 8)) m = tokens / (148 * 8);
-    if (n < m) n = m;
+// The split of a block's lane groups into heads and tokens, and the tokens per
+// tile.  HS is the number that leaves the fewest group steps empty over the
+// heads; a tile is U TS tokens, fewer where that would leave SMs without one.
+void tile_shape(NormArgs& a, int rows) {
+  const int H = a.Hq + a.Hk, groups = kNormThreads / lane_group(a.d);
+  int best = 1;
+  int64_t most = 0;
+  for (int hs = 1; hs <= groups && hs <= H; ++hs) {
+    // heads per step and group, times 2^20
+    const int64_t used = ((int64_t)H << 20) / ((H + hs - 1) / hs) * (groups / hs) / groups;
+    if (used >= most) {
+      most = used;
+      best = hs;
+    }
   }
+  a.hs = best;
+  a.ts = groups / best;
+  const int even = a.tokens / (148 * 4);  // a tile for every resident block
+  if (even < a.ts) {
+    a.hs = groups < H ? groups : H;
+    a.ts = 1;
+  }
+  int n = rows * a.ts;
+  if (n > even) n = even;
   if (n > kMaxTokens) n = kMaxTokens;
-  return n < 1 ? 1 : n;
+  a.per_block = n < 1 ? 1 : n;
 }
 
 constexpr int kFwdBlocks = 148 * 4, kBwdBlocks = 148 * 2;  // as many as are resident
-int bwd_blocks(int tokens, int per_block) {
-  const int64_t n = ((int64_t)tokens + per_block - 1) / per_block;
-  return (int)(n < kBwdBlocks ? n : kBwdBlocks);
-}
-
-size_t table_bytes(const NormArgs& a) { return 2 * sizeof(float2) * (size_t)a.per_block * (a.rot / 2); }
+size_t table_bytes(const NormArgs& a) { return 2 * sizeof(float) * (size_t)a.per_block * a.rot; }
 
 template <typename Tin, int ROT>
 cudaError_t dispatch_fwd_rot(const NormArgs& a, cudaStream_t st) {
@@ -513,7 +533,7 @@ NormArgs norm_args(const void* q, int64_t q_stride, const void* k, int64_t k_str
   a.c = norm == KDA_NORM_RMS ? 1.0f / (float)d : 1.0f;
   a.eps = eps;
   a.pairs = rotation == KDA_ROT_PAIRS;
-  a.per_block = tokens_per_block(tokens, Hq + Hk, d, rot_dim);
+
   return a;
 }
 
@@ -555,6 +575,7 @@ kda_status kda_qk_norm_fwd(const void* q, int64_t q_stride, const void* k, int64
                          tokens, Hq, Hk, d, rot_dim, norm, rotation, eps);
   a.q_out = q_out;
   a.k_out = k_out;
+  tile_shape(a, in_dtype == KDA_BF16 ? kRows<__nv_bfloat16> : kRows<float>);
   cudaStream_t st = (cudaStream_t)stream;
   const cudaError_t e = in_dtype == KDA_BF16 ? dispatch_fwd<__nv_bfloat16>(a, st)
                                              : dispatch_fwd<float>(a, st);
@@ -565,8 +586,7 @@ size_t kda_qk_norm_bwd_workspace_size(int tokens, int Hq, int Hk, int d) {
   if (tokens <= 0 || Hq <= 0 || Hk <= 0 || d <= 0 || d % 8 != 0 || d > 256 || Hq > (1 << 16) ||
       Hk > (1 << 16))
     return 0;
-  // without a rotation a block takes the fewest tokens
-  return sizeof(float) * (size_t)bwd_blocks(tokens, tokens_per_block(tokens, Hq + Hk, d, 0)) * 2 * d;
+  return sizeof(float) * (size_t)(tokens < kBwdBlocks ? tokens : kBwdBlocks) * 2 * d;
 }
 
 kda_status kda_qk_norm_bwd(const void* q, int64_t q_stride, const void* k, int64_t k_stride,
@@ -612,7 +632,9 @@ kda_status kda_qk_norm_bwd(const void* q, int64_t q_stride, const void* k, int64
   a.dq = dq;
   a.dk = dk;
   a.partial = sums ? static_cast<float*>(workspace) : nullptr;
-  a.blocks = bwd_blocks(tokens, a.per_block);
+  tile_shape(a, kBwdRows);
+  const int64_t tiles = ((int64_t)tokens + a.per_block - 1) / a.per_block;
+  a.blocks = (int)(tiles < kBwdBlocks ? tiles : kBwdBlocks);
   cudaStream_t st = (cudaStream_t)stream;
   cudaError_t e = in_dtype == KDA_BF16 ? dispatch_bwd<__nv_bfloat16>(a, st)
                                        : dispatch_bwd<float>(a, st);

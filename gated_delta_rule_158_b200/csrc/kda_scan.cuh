@@ -116,23 +116,6 @@ __device__ __forceinline__ Channels channels_of(const Args& a, int cb) {
 }
 inline int channel_blocks(int D, int G, int CT) { return G * ((D / G + CT - 1) / CT); }
 
-// 2 N consecutive floats as N pairs (aligned to their size)
-template <int N>
-__device__ __forceinline__ void load_pairs(const float* p, f2 (&v)[N]) {
-  if constexpr (N == 1) {
-    v[0] = *reinterpret_cast<const f2*>(p);
-  } else {
-    const ulonglong2 u = *reinterpret_cast<const ulonglong2*>(p);
-    v[0] = u.x;
-    v[1] = u.y;
-  }
-}
-template <int N>
-__device__ __forceinline__ void store_pairs(float* p, const f2 (&v)[N]) {
-  if constexpr (N == 1) *reinterpret_cast<f2*>(p) = v[0];
-  else *reinterpret_cast<ulonglong2*>(p) = make_ulonglong2(v[0], v[1]);
-}
-
 // log(1 + u) for 0 <= u <= 1 as u P(u): P is the polynomial of degree 8 nearest
 // to log(1 + u) / u in relative error (weighted least squares on 4000 Chebyshev
 // points, the weights raised where the error is largest until it is level:
