@@ -35,6 +35,8 @@ KDA_NORM_L2 = 1
 KDA_ROT_HALVES = 0
 KDA_ROT_PAIRS = 1
 
+_current_raw_stream = torch._C._cuda_getCurrentRawStream
+
 _VP = ctypes.c_void_p
 _I = ctypes.c_int
 _I64 = ctypes.c_int64
@@ -160,7 +162,7 @@ def _ptr(t):
 def _stream(stream):
     if stream is None:
         # the handle alone: building a Stream object costs 3 us a call
-        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+        return _current_raw_stream(torch.cuda.current_device())
     if isinstance(stream, torch.cuda.Stream):
         return stream.cuda_stream
     return int(stream)
@@ -378,7 +380,9 @@ def _arg(dev, name, t, shape, dtype, optional=False):
     this shape and type on device `dev`, the current one."""
     if t is None and optional:
         return None
-    _on_device(dev, name, t, shape, dtype)
+    if not isinstance(t, torch.Tensor) or t.dtype is not dtype or t.shape != shape \
+            or t.get_device() != dev:
+        _on_device(dev, name, t, shape, dtype)
     if not t.is_contiguous():
         raise ValueError(f"{name}: expected a dense tensor")
     return t.data_ptr()
@@ -404,10 +408,12 @@ def _like(t):
 def _rows(dev, name, t, shape, lead, dtype):
     """(pointer, row stride) of a tensor whose first `lead` dimensions number
     its rows: rows dense, any constant distance apart."""
-    _on_device(dev, name, t, shape, dtype)
+    if not isinstance(t, torch.Tensor) or t.dtype is not dtype or t.shape != shape \
+            or t.get_device() != dev:
+        _on_device(dev, name, t, shape, dtype)
     if t.is_contiguous():
-        width = 1
-        for n in shape[lead:]:
+        width = shape[lead]
+        for n in shape[lead + 1:]:
             width *= n
         return t.data_ptr(), width
     strides, width = t.stride(), 1

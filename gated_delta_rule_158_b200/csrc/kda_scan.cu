@@ -686,7 +686,7 @@ Segments plan_segments(const int32_t* cu, int num_seqs, int B, int T, int D, int
   int64_t len = T;
   if (cu) {
     m.wide = true;
-    len = 3 * T * per_seq / (kSms * 16);
+    len = 4 * T * per_seq / (kSms * 16);
     if (len < 256) len = 256;
   } else {
     m.wide = warps >= kSms * 8;
