@@ -244,7 +244,7 @@ __global__ void __launch_bounds__(Layout<S, SC_>::NT) scan_fwd_kernel(const Args
       for (int q = 0; q < SC; ++q)
 #pragma unroll
         for (int p = 0; p < 2; ++p)
-          g.w[k][q][p] = pack2(ex2(g.dt[k][q] * A2[q][2 * p]), ex2(g.dt[k][q] * A2[q][2 * p + 1]));
+          g.w[k][q][p] = pack2(decay(g.dt[k][q], A2[q][2 * p]), decay(g.dt[k][q], A2[q][2 * p + 1]));
   };
   auto apply = [&](const Pair& g, float (&y)[SC][4], int at) {
 #pragma unroll
@@ -463,6 +463,8 @@ __global__ void __launch_bounds__(256) scan_step_kernel(const Args a, float* sta
     if (a.delta_bias) dt[0] += a.delta_bias[d];
   }
   if (ns > 0) load_vec<float, 4>(a.A + so, A2);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) A2[i] *= kLog2e;
   step_sizes<1>(dt, a.softplus);
   const float u = dt[0] * x;
   float y[4] = {};
@@ -470,10 +472,9 @@ __global__ void __launch_bounds__(256) scan_step_kernel(const Args a, float* sta
   for (int k = 0; k < NSEQ; ++k) {
     const float sk = NSEQ == 1 ? dt[0] : __shfl_sync(0xffffffffu, dt[0], k, LN);
     const float uk = NSEQ == 1 ? u : __shfl_sync(0xffffffffu, u, k, LN);
-    const float sl = sk * kLog2e;
     const f2 uu = pack2(uk, uk);
-    const f2 w0 = pack2(ex2(sl * A2[0]), ex2(sl * A2[1]));
-    const f2 w1 = pack2(ex2(sl * A2[2]), ex2(sl * A2[3]));
+    const f2 w0 = pack2(decay(sk, A2[0]), decay(sk, A2[1]));
+    const f2 w1 = pack2(decay(sk, A2[2]), decay(sk, A2[3]));
     h[k][0] = fma2(w0, h[k][0], mul2(uu, pack2(b[k].at(0), b[k].at(1))));
     h[k][1] = fma2(w1, h[k][1], mul2(uu, pack2(b[k].at(2), b[k].at(3))));
     if (k < ns) store_pairs<2>(state + (n0 + k) * ds + so, h[k]);

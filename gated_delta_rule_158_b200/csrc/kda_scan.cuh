@@ -116,6 +116,18 @@ __device__ __forceinline__ Channels channels_of(const Args& a, int cb) {
 }
 inline int channel_blocks(int D, int G, int CT) { return G * ((D / G + CT - 1) / CT); }
 
+// The decay e^{dt A} as 2^(dt A2 + kNudge), A2 = A log2 e.  Over a state's memory
+// of 1 / (dt |A|) tokens a mean error of the exponential adds up where its
+// scatter does not, and the unit's results lie 2.0e-8 of themselves low on
+// average for decays of 0.001 to 1 (measured on a B200 over 8 M values a decade;
+// rms error 3.7e-8): the exponent is raised by that much.  dt = 0 still gives
+// exactly 1.
+constexpr float kNudge = 2.9e-8f;
+__device__ __forceinline__ float decay(float dt, float A2) { return ex2(fmaf(dt, A2, kNudge)); }
+__device__ __forceinline__ f2 decay_exp(f2 dt, f2 A2) {
+  return fma2(dt, A2, pack2(kNudge, kNudge));
+}
+
 // log(1 + u) for 0 <= u <= 1 as u P(u): P is the polynomial of degree 8 nearest
 // to log(1 + u) / u in relative error (weighted least squares on 4000 Chebyshev
 // points, the weights raised where the error is largest until it is level:

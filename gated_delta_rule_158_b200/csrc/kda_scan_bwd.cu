@@ -169,12 +169,12 @@ __global__ void __launch_bounds__(Walk<S>::NT, Walk<S>::kCtas) scan_bwd_kernel(c
   const int64_t ds = (int64_t)a.D * S;
   const int64_t so = (int64_t)d * S + nl * 4;
 
-  f2 A2[2][2], carry[2][2], dA[2][2];
+  f2 A2[2][2], carry[2][2], dA[2][2], dA_err[2][2];
   float* const own_hin = sm + L::kHin + tid * 4;  // of channel q: + 4 q NT
 #pragma unroll
   for (int q = 0; q < 2; ++q)
 #pragma unroll
-    for (int i = 0; i < 2; ++i) A2[q][i] = carry[q][i] = dA[q][i] = zero2();
+    for (int i = 0; i < 2; ++i) A2[q][i] = carry[q][i] = dA[q][i] = dA_err[q][i] = zero2();
   if (live) {
     const float* from = a.split ? a.g_seg + un.slot * ds : a.d_final ? a.d_final + un.n * ds : nullptr;
 #pragma unroll
@@ -306,7 +306,7 @@ __global__ void __launch_bounds__(Walk<S>::NT, Walk<S>::kCtas) scan_bwd_kernel(c
     const float* pb = sm + L::kB + s * S + nl * 4;
     const float* pc = sm + L::kC + s * S + nl * 4;
     float* red = sm + L::kRed + ((tid >> 5) * T + s) * 2 * S;
-    f2 h0[2][2], hs[kStep][2][2];
+    f2 h0[2][2], hs[kStep][2][2], dAs[2][2];
 #pragma unroll
     for (int q = 0; q < 2; ++q) {
       load_pairs<2>(keep_at(step, q), h0[q]);
@@ -332,7 +332,7 @@ __global__ void __launch_bounds__(Walk<S>::NT, Walk<S>::kCtas) scan_bwd_kernel(c
         const f2 dd = pack2(dt[q], dt[q]), uu = pack2(u[q], u[q]);
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
-          hs[t][q][k] = fma2(ex2_2(mul2(dd, A2[q][k])),
+          hs[t][q][k] = fma2(ex2_2(decay_exp(dd, A2[q][k])),
                              t == 0 ? h0[q][k] : hs[t > 0 ? t - 1 : 0][q][k], mul2(uu, b[k]));
         }
       }
@@ -367,9 +367,9 @@ __global__ void __launch_bounds__(Walk<S>::NT, Walk<S>::kCtas) scan_bwd_kernel(c
             pC[k] = q == 0 ? mul2(hs[t][q][k], dy) : fma2(hs[t][q][k], dy, pC[k]);
             sB = k == 0 ? mul2(g, b[k]) : fma2(g, b[k], sB);
             sy = k == 0 ? mul2(cc[k], hs[t][q][k]) : fma2(cc[k], hs[t][q][k], sy);
-            carry[q][k] = mul2(g, ex2_again(mul2(dd, A2[q][k])));
+            carry[q][k] = mul2(g, ex2_again(decay_exp(dd, A2[q][k])));
             const f2 ga = mul2(carry[q][k], hp);
-            dA[q][k] = fma2(ga, dd, dA[q][k]);
+            dAs[q][k] = t == kStep - 1 ? mul2(ga, dd) : fma2(ga, dd, dAs[q][k]);
             sA = k == 0 ? mul2(ga, A2[q][k]) : fma2(ga, A2[q][k], sA);
           }
           gA[q] = sum2(sA);
@@ -400,6 +400,18 @@ __global__ void __launch_bounds__(Walk<S>::NT, Walk<S>::kCtas) scan_bwd_kernel(c
         if (nl < 2) pdy[(t4 + m) * CT + nl] = y[m];
       }
     }
+    // a segment's tokens are many: the steps' sums are added with the rounding
+    // error of each addition carried along
+#pragma unroll
+    for (int q = 0; q < 2; ++q)
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const f2 neg = pack2(-1.f, -1.f);
+        const f2 v = fma2(dA_err[q][k], neg, dAs[q][k]);
+        const f2 s = add2(dA[q][k], v);
+        dA_err[q][k] = fma2(v, neg, fma2(dA[q][k], neg, s));
+        dA[q][k] = s;
+      }
   };
   auto finish_tile = [&](int i) {
     float skip[VEC] = {}, bias[VEC] = {};
