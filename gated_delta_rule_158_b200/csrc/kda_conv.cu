@@ -109,6 +109,13 @@ __device__ __forceinline__ Run run_at(const ConvArgs& a, int t) {
     r.n = find_range(a.cu, a.num_seqs, t);
     r.start = __ldg(a.cu + r.n);
     r.end = __ldg(a.cu + r.n + 1);
+    // (debug builds) a run outside the batch ends at its token: nothing beyond
+    // is read
+    if (!in_bounds(a.sb, r.end, a.total + 1, kSiteConvRun) ||
+        !in_bounds(a.sb, t, r.end, kSiteConvRun)) {
+      r.start = t;
+      r.end = t + 1;
+    }
   } else {
     r.n = t / a.T;
     r.start = r.n * a.T;

@@ -53,6 +53,9 @@ enum BoundsSite : int32_t {
   kSiteSimtStateSlot = 0xB202, // chunk_simt_kernel: state slot
   kSiteBwdUnitRows = 0xB401,   // backward: a unit's rows within the batch
   kSiteBwdChunks = 0xB402,     // backward: a unit's chunk slice of the workspace
+  kSiteScanUnitRows = 0xB501,  // selective scan: a segment's rows within the batch
+  kSiteScanSlot = 0xB502,      // selective scan: its slot in the workspace
+  kSiteConvRun = 0xB601,       // short convolution: a run's rows within the batch
 };
 
 // --------------------------------------------------------------- element io

@@ -28,7 +28,7 @@ struct Unit {
   bool valid;
 };
 
-__device__ __forceinline__ Unit resolve(const Segments& m, const StatusBlock* sb, int unit) {
+__device__ __forceinline__ Unit resolve(const Segments& m, StatusBlock* sb, int unit) {
   Unit u;
   int64_t start, end;
   int k, len = m.seg_len;
@@ -56,6 +56,10 @@ __device__ __forceinline__ Unit resolve(const Segments& m, const StatusBlock* sb
   u.first = k == 0;
   u.t0 = start + (int64_t)k * len;
   u.t1 = u.last ? end : u.t0 + len;
+  if (m.cu)
+    u.valid = in_bounds(sb, u.t1, (int64_t)m.T + 1, kSiteScanUnitRows) &&
+              in_bounds(sb, u.t0, u.t1 + 1, kSiteScanUnitRows) &&
+              in_bounds(sb, u.slot, m.units, kSiteScanSlot);
   return u;
 }
 

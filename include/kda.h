@@ -39,8 +39,10 @@
  *    slots), the rows of o a chunk stores, the backward's per-chunk workspace
  *    slices and gradient rows.  A failed check records KDA_ERR_BOUNDS (detail:
  *    the check site) in the workspace status word and the access is skipped;
- *    nothing traps.  The decode kernels (no workspace, no status word) are not
- *    instrumented.  Release builds compile the checks away.
+ *    nothing traps.  The selective scan checks the rows and the workspace slot
+ *    of a segment, the short convolution the rows of a run.  The decode kernels
+ *    (no workspace, no status word) are not instrumented.  Release builds
+ *    compile the checks away.
  */
 #ifndef LIBKDA_KDA_H_
 #define LIBKDA_KDA_H_
