@@ -6,6 +6,7 @@ and the current CUDA stream through unchanged.  No computation happens here;
 if libkda.so is missing or fails to load, every call raises.
 """
 import ctypes
+import math
 import os
 
 import torch
@@ -367,28 +368,32 @@ def kda_recurrent_bwd(q, k, v, g, beta, dout, grads, workspace, init_state=None,
 
 
 # ---- the operators around the recurrence: their inputs may be row slices of
-# wider tensors, so shapes, types and devices are checked here
-
-# (tuples of types and shapes are compared as they are: these checks run on
-# every call of a decode loop)
+# wider tensors, so shapes, types and devices are checked here.  A decode loop
+# makes these calls once per layer and token, and the checks are most of a
+# call's host time: they ask one question per tensor and explain a no later.
 
 _F32T = torch.float32
 
 
-def _arg(dev, name, t, shape, dtype, optional=False):
-    """The tensor's pointer, after checking that it is a dense CUDA tensor of
-    this shape and type on device `dev`, the current one."""
-    if t is None and optional:
-        return None
-    if not isinstance(t, torch.Tensor) or t.dtype is not dtype or t.shape != shape \
-            or t.get_device() != dev:
-        _on_device(dev, name, t, shape, dtype)
-    if not t.is_contiguous():
-        raise ValueError(f"{name}: expected a dense tensor")
-    return t.data_ptr()
+def _arg(dev, name, t, shape, dtype):
+    """The pointer of a dense CUDA tensor of this shape and type on device
+    `dev`, the current one."""
+    try:
+        if t.dtype is dtype and t.shape == shape and t.get_device() == dev \
+                and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:
+        pass
+    _refuse(dev, name, t, shape, dtype)
+    raise ValueError(f"{name}: expected a dense tensor")
 
 
-def _on_device(dev, name, t, shape, dtype):
+def _opt(dev, name, t, shape, dtype):
+    return None if t is None else _arg(dev, name, t, shape, dtype)
+
+
+def _refuse(dev, name, t, shape, dtype):
+    """Raises what is wrong with the tensor, if it is not its strides."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name}: expected a torch.Tensor")
     if t.dtype is not dtype:
@@ -399,28 +404,22 @@ def _on_device(dev, name, t, shape, dtype):
         raise ValueError(f"{name}: expected a tensor on the current CUDA device")
 
 
-def _like(t):
-    """The type of a tensor that has to have t's element type."""
-    _dtype(t)
-    return t.dtype
-
-
-def _rows(dev, name, t, shape, lead, dtype):
+def _rows(dev, name, t, shape, lead, width, dtype):
     """(pointer, row stride) of a tensor whose first `lead` dimensions number
-    its rows: rows dense, any constant distance apart."""
-    if not isinstance(t, torch.Tensor) or t.dtype is not dtype or t.shape != shape \
-            or t.get_device() != dev:
-        _on_device(dev, name, t, shape, dtype)
-    if t.is_contiguous():
-        width = shape[lead]
-        for n in shape[lead + 1:]:
-            width *= n
-        return t.data_ptr(), width
-    strides, width = t.stride(), 1
+    its rows of `width` elements: rows dense, any constant distance apart."""
+    try:
+        if t.dtype is dtype and t.shape == shape and t.get_device() == dev:
+            if t.is_contiguous():
+                return t.data_ptr(), width
+        else:
+            _refuse(dev, name, t, shape, dtype)
+    except AttributeError:
+        _refuse(dev, name, t, shape, dtype)
+    strides, dense = t.stride(), 1
     for n, st in zip(reversed(shape[lead:]), reversed(strides[lead:])):
-        if n > 1 and st != width:
+        if n > 1 and st != dense:
             raise ValueError(f"{name}: rows must be dense")
-        width *= n
+        dense *= n
     stride = None
     for n, st in zip(reversed(shape[:lead]), reversed(strides[:lead])):
         if n == 1:
@@ -438,8 +437,13 @@ def _rows(dev, name, t, shape, lead, dtype):
     return t.data_ptr(), stride
 
 
-def _grad(dev, grads, name, shape, optional=False):
-    return _arg(dev, f"grads['{name}']", grads.get(name), shape, _F32T, optional)
+def _grad(dev, grads, name, shape):
+    return _arg(dev, f"grads['{name}']", grads.get(name), shape, _F32T)
+
+
+def _opt_grad(dev, grads, name, shape):
+    t = grads.get(name)
+    return None if t is None else _arg(dev, f"grads['{name}']", t, shape, _F32T)
 
 
 def _offsets(dev, cu_seqlens, batch):
@@ -453,8 +457,13 @@ def _offsets(dev, cu_seqlens, batch):
 def _scratch(dev, workspace):
     if workspace is None:
         return None, 0
-    _on_device(dev, "workspace", workspace, workspace.shape, workspace.dtype)
-    return _ptr(workspace), workspace.numel() * workspace.element_size()
+    return (_arg(dev, "workspace", workspace, workspace.shape, workspace.dtype),
+            workspace.numel() * workspace.element_size())
+
+
+def _on(stream, dev):
+    # the current stream's handle alone: building a Stream object costs 3 us
+    return _current_raw_stream(dev) if stream is None else _stream(stream)
 
 
 def kda_short_conv_fwd(x, weight, out, workspace, bias=None, init_state=None, cu_seqlens=None,
@@ -463,31 +472,31 @@ def kda_short_conv_fwd(x, weight, out, workspace, bias=None, init_state=None, cu
     (rows may be slices of a wider tensor), weight fp32 [D,W], out [B,T,D],
     states [N,W-1,D] of x's type."""
     dev = torch.cuda.current_device()
-    B, T, D = x.shape
+    shape, dt, code = x.shape, x.dtype, _dtype(x)
+    B, T, D = shape
     W = weight.shape[-1]
-    dt = _like(x)
     cu, num, N = _offsets(dev, cu_seqlens, B)
-    xp, xs = _rows(dev, "x", x, (B, T, D), 2, dt)
+    xp, xs = _rows(dev, "x", x, shape, 2, D, dt)
     ws, wsb = _scratch(dev, workspace)
     _check(lib().kda_short_conv_fwd(
-        xp, xs, _arg(dev, "weight", weight, (D, W), _F32T), _arg(dev, "bias", bias, (D,), _F32T, True),
-        _dtype(x), _arg(dev, "init_state", init_state, (N, W - 1, D), dt, True), cu, num, B, T, D, W,
-        int(activation), _arg(dev, "out", out, (B, T, D), dt),
-        _arg(dev, "final_state", final_state, (N, W - 1, D), dt, True), ws, wsb, _stream(stream)),
+        xp, xs, _arg(dev, "weight", weight, (D, W), _F32T), _opt(dev, "bias", bias, (D,), _F32T),
+        code, _opt(dev, "init_state", init_state, (N, W - 1, D), dt), cu, num, B, T, D, W,
+        activation, _arg(dev, "out", out, shape, dt),
+        _opt(dev, "final_state", final_state, (N, W - 1, D), dt), ws, wsb, _on(stream, dev)),
         "kda_short_conv_fwd")
 
 
 def kda_short_conv_step(x, weight, state, out, bias=None, activation=KDA_ACT_SILU, stream=None):
     """One token of N sequences: x, out [N,D], state [N,W-1,D] shifted in place."""
     dev = torch.cuda.current_device()
-    N, D = x.shape
+    shape, dt, code = x.shape, x.dtype, _dtype(x)
+    N, D = shape
     W = weight.shape[-1]
-    dt = _like(x)
-    xp, xs = _rows(dev, "x", x, (N, D), 1, dt)
+    xp, xs = _rows(dev, "x", x, shape, 1, D, dt)
     _check(lib().kda_short_conv_step(
-        xp, xs, _arg(dev, "weight", weight, (D, W), _F32T), _arg(dev, "bias", bias, (D,), _F32T, True),
-        _dtype(x), _arg(dev, "state", state, (N, W - 1, D), dt), N, D, W, int(activation),
-        _arg(dev, "out", out, (N, D), dt), _stream(stream)), "kda_short_conv_step")
+        xp, xs, _arg(dev, "weight", weight, (D, W), _F32T), _opt(dev, "bias", bias, (D,), _F32T),
+        code, _arg(dev, "state", state, (N, W - 1, D), dt), N, D, W, activation,
+        _arg(dev, "out", out, shape, dt), _on(stream, dev)), "kda_short_conv_step")
 
 
 def kda_short_conv_bwd_workspace_size(B, T, D, W, num_seqs=0) -> int:
@@ -500,19 +509,20 @@ def kda_short_conv_bwd(x, weight, dout, grads, workspace, bias=None, init_state=
     fp32 outputs dx [B,T,D], dweight [D,W] and optionally dbias [D], d_init
     [N,W-1,D]."""
     dev = torch.cuda.current_device()
-    B, T, D = x.shape
+    shape, dt, code = x.shape, x.dtype, _dtype(x)
+    B, T, D = shape
     W = weight.shape[-1]
     cu, num, N = _offsets(dev, cu_seqlens, B)
-    xp, xs = _rows(dev, "x", x, (B, T, D), 2, _like(x))
+    xp, xs = _rows(dev, "x", x, shape, 2, D, dt)
     ws, wsb = _scratch(dev, workspace)
     _check(lib().kda_short_conv_bwd(
-        xp, xs, _arg(dev, "weight", weight, (D, W), _F32T), _arg(dev, "bias", bias, (D,), _F32T, True),
-        _dtype(x), _arg(dev, "init_state", init_state, (N, W - 1, D), x.dtype, True),
-        _arg(dev, "dout", dout, (B, T, D), _F32T),
-        _arg(dev, "d_final", d_final, (N, W - 1, D), _F32T, True), cu, num, B, T, D, W,
-        int(activation), _grad(dev, grads, "dx", (B, T, D)), _grad(dev, grads, "dweight", (D, W)),
-        _grad(dev, grads, "dbias", (D,), True), _grad(dev, grads, "d_init", (N, W - 1, D), True), ws, wsb,
-        _stream(stream)), "kda_short_conv_bwd")
+        xp, xs, _arg(dev, "weight", weight, (D, W), _F32T), _opt(dev, "bias", bias, (D,), _F32T),
+        code, _opt(dev, "init_state", init_state, (N, W - 1, D), dt),
+        _arg(dev, "dout", dout, shape, _F32T),
+        _opt(dev, "d_final", d_final, (N, W - 1, D), _F32T), cu, num, B, T, D, W, activation,
+        _grad(dev, grads, "dx", shape), _grad(dev, grads, "dweight", (D, W)),
+        _opt_grad(dev, grads, "dbias", (D,)), _opt_grad(dev, grads, "d_init", (N, W - 1, D)), ws,
+        wsb, _on(stream, dev)), "kda_short_conv_bwd")
 
 
 def kda_selective_scan_fwd_workspace_size(B, T, D, S, G=1, num_seqs=0) -> int:
@@ -521,16 +531,16 @@ def kda_selective_scan_fwd_workspace_size(B, T, D, S, G=1, num_seqs=0) -> int:
 
 def _scan_inputs(dev, x, delta, A, Bm, Cm, D, z, delta_bias, delta_softplus):
     """The marshalled input arguments that the scan's entries share."""
-    lead, ch = tuple(x.shape[:-1]), x.shape[-1]
-    S, G = A.shape[-1], Bm.shape[-2]
-    n, dt = len(lead), _like(x)
-    args = [*_rows(dev, "x", x, (*lead, ch), n, dt), *_rows(dev, "delta", delta, (*lead, ch), n, dt),
-            _arg(dev, "A", A, (ch, S), _F32T), *_rows(dev, "Bm", Bm, (*lead, G, S), n, dt),
-            *_rows(dev, "Cm", Cm, (*lead, G, S), n, dt), _arg(dev, "D", D, (ch,), _F32T, True),
-            *((None, 0) if z is None else _rows(dev, "z", z, (*lead, ch), n, dt)),
-            _arg(dev, "delta_bias", delta_bias, (ch,), _F32T, True), int(bool(delta_softplus)),
-            _dtype(x)]
-    return args, ch, S, G
+    shape, dt, code = x.shape, x.dtype, _dtype(x)
+    n, ch = len(shape) - 1, shape[-1]
+    (S,), (G,) = A.shape[-1:], Bm.shape[-2:-1]
+    mix, w = (*shape[:-1], G, S), G * S
+    return (*_rows(dev, "x", x, shape, n, ch, dt), *_rows(dev, "delta", delta, shape, n, ch, dt),
+            _arg(dev, "A", A, (ch, S), _F32T), *_rows(dev, "Bm", Bm, mix, n, w, dt),
+            *_rows(dev, "Cm", Cm, mix, n, w, dt), _opt(dev, "D", D, (ch,), _F32T),
+            *((None, 0) if z is None else _rows(dev, "z", z, shape, n, ch, dt)),
+            _opt(dev, "delta_bias", delta_bias, (ch,), _F32T), 1 if delta_softplus else 0,
+            code), ch, S, G
 
 
 def kda_selective_scan_fwd(x, delta, A, Bm, Cm, out, workspace, D=None, z=None, delta_bias=None,
@@ -545,9 +555,9 @@ def kda_selective_scan_fwd(x, delta, A, Bm, Cm, out, workspace, D=None, z=None, 
     cu, num, N = _offsets(dev, cu_seqlens, B)
     ws, wsb = _scratch(dev, workspace)
     _check(lib().kda_selective_scan_fwd(
-        *args, _arg(dev, "init_state", init_state, (N, ch, S), _F32T, True), cu, num, B, T, ch, S, G,
+        *args, _opt(dev, "init_state", init_state, (N, ch, S), _F32T), cu, num, B, T, ch, S, G,
         _arg(dev, "out", out, (B, T, ch), x.dtype),
-        _arg(dev, "final_state", final_state, (N, ch, S), _F32T, True), ws, wsb, _stream(stream)),
+        _opt(dev, "final_state", final_state, (N, ch, S), _F32T), ws, wsb, _on(stream, dev)),
         "kda_selective_scan_fwd")
 
 
@@ -556,11 +566,11 @@ def kda_selective_scan_step(x, delta, A, Bm, Cm, state, out, D=None, z=None, del
     """One token of N sequences: x, delta, z, out [N,D], Bm, Cm [N,G,S], state
     fp32 [N,D,S] in place."""
     dev = torch.cuda.current_device()
-    N = x.shape[0]
     args, ch, S, G = _scan_inputs(dev, x, delta, A, Bm, Cm, D, z, delta_bias, delta_softplus)
+    N = x.shape[0]
     _check(lib().kda_selective_scan_step(
         *args, _arg(dev, "state", state, (N, ch, S), _F32T), N, ch, S, G,
-        _arg(dev, "out", out, (N, ch), x.dtype), _stream(stream)), "kda_selective_scan_step")
+        _arg(dev, "out", out, (N, ch), x.dtype), _on(stream, dev)), "kda_selective_scan_step")
 
 
 def kda_selective_scan_bwd_workspace_size(B, T, D, S, G=1, num_seqs=0) -> int:
@@ -578,32 +588,33 @@ def kda_selective_scan_bwd(x, delta, A, Bm, Cm, dout, grads, workspace, D=None, 
     args, ch, S, G = _scan_inputs(dev, x, delta, A, Bm, Cm, D, z, delta_bias, delta_softplus)
     cu, num, N = _offsets(dev, cu_seqlens, B)
     ws, wsb = _scratch(dev, workspace)
+    rows, mix, state = (B, T, ch), (B, T, G, S), (N, ch, S)
     _check(lib().kda_selective_scan_bwd(
-        *args, _arg(dev, "init_state", init_state, (N, ch, S), _F32T, True),
-        _arg(dev, "dout", dout, (B, T, ch), x.dtype),
-        _arg(dev, "d_final", d_final, (N, ch, S), _F32T, True), cu, num, B, T, ch, S, G,
-        _grad(dev, grads, "dx", (B, T, ch)), _grad(dev, grads, "ddelta", (B, T, ch)),
-        _grad(dev, grads, "dA", (ch, S)), _grad(dev, grads, "dB", (B, T, G, S)),
-        _grad(dev, grads, "dC", (B, T, G, S)), _grad(dev, grads, "dD", (ch,), True),
-        _grad(dev, grads, "dz", (B, T, ch), z is None), _grad(dev, grads, "ddelta_bias", (ch,), True),
-        _grad(dev, grads, "d_init", (N, ch, S), True), ws, wsb, _stream(stream)),
+        *args, _opt(dev, "init_state", init_state, state, _F32T),
+        _arg(dev, "dout", dout, rows, x.dtype), _opt(dev, "d_final", d_final, state, _F32T), cu,
+        num, B, T, ch, S, G, _grad(dev, grads, "dx", rows), _grad(dev, grads, "ddelta", rows),
+        _grad(dev, grads, "dA", (ch, S)), _grad(dev, grads, "dB", mix),
+        _grad(dev, grads, "dC", mix), _opt_grad(dev, grads, "dD", (ch,)),
+        _opt_grad(dev, grads, "dz", rows), _opt_grad(dev, grads, "ddelta_bias", (ch,)),
+        _opt_grad(dev, grads, "d_init", state), ws, wsb, _on(stream, dev)),
         "kda_selective_scan_bwd")
 
 
 def _norm_inputs(dev, q, k, q_weight, k_weight, positions, inv_freq, mode, rotation, eps):
-    lead, dim, dt = tuple(q.shape[:-2]), q.shape[-1], _like(q)
-    Hq, Hk, n = q.shape[-2], k.shape[-2], len(lead)
-    tokens = 1
-    for m in lead:
-        tokens *= m
+    """The marshalled input arguments that the norms' entries share, and the
+    shapes of q and k."""
+    shape, dt, code = q.shape, q.dtype, _dtype(q)
+    *lead, Hq, dim = shape
+    Hk = k.shape[-2]
+    k_shape, n, tokens = (*lead, Hk, dim), len(lead), math.prod(lead)
     rot = 0 if inv_freq is None else 2 * inv_freq.numel()
-    args = [*_rows(dev, "q", q, (*lead, Hq, dim), n, dt), *_rows(dev, "k", k, (*lead, Hk, dim), n, dt),
-            _arg(dev, "q_weight", q_weight, (dim,), _F32T, True),
-            _arg(dev, "k_weight", k_weight, (dim,), _F32T, True),
-            _arg(dev, "positions", positions, lead, torch.int32, True),
-            _arg(dev, "inv_freq", inv_freq, (rot // 2,), _F32T, True), _dtype(q), tokens, Hq, Hk, dim,
-            rot, int(mode), int(rotation), float(eps)]
-    return args, lead, Hq, Hk, dim
+    return (*_rows(dev, "q", q, shape, n, Hq * dim, dt),
+            *_rows(dev, "k", k, k_shape, n, Hk * dim, dt),
+            _opt(dev, "q_weight", q_weight, (dim,), _F32T),
+            _opt(dev, "k_weight", k_weight, (dim,), _F32T),
+            _opt(dev, "positions", positions, shape[:-2], torch.int32),
+            _opt(dev, "inv_freq", inv_freq, (rot // 2,), _F32T), code, tokens, Hq, Hk, dim, rot,
+            mode, rotation, eps), shape, k_shape
 
 
 def kda_qk_norm_fwd(q, k, q_out, k_out, q_weight=None, k_weight=None, positions=None,
@@ -614,11 +625,11 @@ def kda_qk_norm_fwd(q, k, q_out, k_out, q_weight=None, k_weight=None, positions=
     (fp32).  q [..., Hq, d], k [..., Hk, d] (rows of a token may be slices of
     a wider tensor); q_out, k_out dense, of the same type, or q, k themselves."""
     dev = torch.cuda.current_device()
-    args, lead, Hq, Hk, dim = _norm_inputs(dev, q, k, q_weight, k_weight, positions, inv_freq, mode,
-                                           rotation, eps)
+    args, qs, ks = _norm_inputs(dev, q, k, q_weight, k_weight, positions, inv_freq, mode,
+                                rotation, eps)
     _check(lib().kda_qk_norm_fwd(
-        *args, _arg(dev, "q_out", q_out, (*lead, Hq, dim), q.dtype),
-        _arg(dev, "k_out", k_out, (*lead, Hk, dim), q.dtype), _stream(stream)), "kda_qk_norm_fwd")
+        *args, _arg(dev, "q_out", q_out, qs, q.dtype), _arg(dev, "k_out", k_out, ks, q.dtype),
+        _on(stream, dev)), "kda_qk_norm_fwd")
 
 
 def kda_qk_norm_bwd_workspace_size(tokens, Hq, Hk, d) -> int:
@@ -632,14 +643,15 @@ def kda_qk_norm_bwd(q, k, dq_out, dk_out, grads, workspace=None, q_weight=None, 
     fp32 outputs dq, dk (dq may be dq_out itself, dk dk_out) and optionally
     dq_weight, dk_weight [d], which need the workspace."""
     dev = torch.cuda.current_device()
-    args, lead, Hq, Hk, dim = _norm_inputs(dev, q, k, q_weight, k_weight, positions, inv_freq, mode,
-                                           rotation, eps)
+    args, qs, ks = _norm_inputs(dev, q, k, q_weight, k_weight, positions, inv_freq, mode,
+                                rotation, eps)
+    dim = qs[-1]
     ws, wsb = _scratch(dev, workspace)
     _check(lib().kda_qk_norm_bwd(
-        *args, _arg(dev, "dq_out", dq_out, (*lead, Hq, dim), _F32T),
-        _arg(dev, "dk_out", dk_out, (*lead, Hk, dim), _F32T), _grad(dev, grads, "dq", (*lead, Hq, dim)),
-        _grad(dev, grads, "dk", (*lead, Hk, dim)), _grad(dev, grads, "dq_weight", (dim,), True),
-        _grad(dev, grads, "dk_weight", (dim,), True), ws, wsb, _stream(stream)), "kda_qk_norm_bwd")
+        *args, _arg(dev, "dq_out", dq_out, qs, _F32T), _arg(dev, "dk_out", dk_out, ks, _F32T),
+        _grad(dev, grads, "dq", qs), _grad(dev, grads, "dk", ks),
+        _opt_grad(dev, grads, "dq_weight", (dim,)), _opt_grad(dev, grads, "dk_weight", (dim,)),
+        ws, wsb, _on(stream, dev)), "kda_qk_norm_bwd")
 
 
 def kda_get_device_status(workspace, stream=None):

@@ -250,20 +250,32 @@ def test_binding_refuses_host_tensors_types_and_shapes(monkeypatch):
                                     torch.zeros(2, 1, 16), torch.zeros(2, 64, 16), x[:, 1])
 
 
-def test_row_strides_of_slices(monkeypatch):
-    monkeypatch.setattr(_lib, "_on_device", lambda *a: None)  # host tensors pass
+def test_row_strides_of_slices():
     wide = torch.zeros(3, 5, 96)
-    f = torch.float32
-    p, st = _lib._rows(0, "x", wide[..., 32:64], (3, 5, 32), 2, f)
+    f, host = torch.float32, wide.get_device()
+
+    def rows(t, lead, width, shape=None):
+        return _lib._rows(host, "x", t, t.shape if shape is None else shape, lead, width, f)
+
+    p, st = rows(wide[..., 32:64], 2, 32)
     assert st == 96 and p == wide.data_ptr() + 32 * 4
-    assert _lib._rows(0, "x", wide[:1, :1], (1, 1, 96), 2, f)[1] == 96  # no second row
-    assert _lib._rows(0, "x", wide[:, 2:3], (3, 1, 96), 2, f)[1] == 480
-    assert _lib._rows(0, "q", wide.view(3, 5, 4, 24)[:, :, 1:3], (3, 5, 2, 24), 2, f)[1] == 96
+    assert rows(wide[:1, :1], 2, 96)[1] == 96  # no second row
+    assert rows(wide[:1, :1, :32], 2, 32)[1] == 32
+    assert rows(wide[:, 2:3], 2, 96)[1] == 480
+    assert rows(wide.view(3, 5, 4, 24)[:, :, 1:3], 2, 48)[1] == 96
     with pytest.raises(ValueError, match="constant distance"):
-        _lib._rows(0, "x", wide[:, :4], (3, 4, 96), 2, f)
+        rows(wide[:, :4], 2, 96)
     with pytest.raises(ValueError, match="dense"):
-        _lib._rows(0, "x", wide[..., ::2], (3, 5, 48), 2, f)
+        rows(wide[..., ::2], 2, 48)
     with pytest.raises(ValueError, match="dense"):
-        _lib._rows(0, "q", wide.view(3, 5, 4, 24)[:, :, ::2], (3, 5, 2, 24), 2, f)
-    with pytest.raises(ValueError):
-        _lib._rows(0, "x", wide[:1, :1].expand(3, 5, 96), (3, 5, 96), 2, f)
+        rows(wide.view(3, 5, 4, 24)[:, :, ::2], 2, 48)
+    with pytest.raises(ValueError, match="overlap"):
+        rows(wide[:1, :1].expand(3, 5, 96), 2, 96)
+    with pytest.raises(ValueError, match="shape"):
+        rows(wide, 2, 96, shape=(3, 5, 95))
+    with pytest.raises(TypeError, match="Tensor"):
+        _lib._rows(host, "x", None, (3, 5, 96), 2, 96, f)
+    with pytest.raises(TypeError, match="Tensor"):
+        _lib._arg(host, "x", [1.0], (1,), f)
+    with pytest.raises(ValueError, match="dense"):
+        _lib._arg(host, "x", wide[..., ::2], (3, 5, 48), f)
