@@ -8,6 +8,13 @@
 // loaded once per strip plus W - 1 rows at its head (which the strip before
 // has just read: L2 hits).  The batch is one flat axis of B * T tokens; a
 // strip that crosses a sequence boundary starts a new run there.
+//
+// Measured on a B200 (6455 GB/s copy): 65,000 packed tokens x 4096 bf16 with
+// SiLU, 194 us = 5.5 TB/s; with rows prefetched to registers instead of the
+// ring it was 230 us, and one product per instruction instead of two (f32x2)
+// made the special-function and issue slots the bound (507 us at eight channels
+// a thread).  One token of 256 sequences x 12,288: 11.2 us, 4.5 TB/s.
+// Gradients of 16,384 x 4096 (x bf16; dout, dx fp32): 114 us = 5.9 TB/s.
 #include "kda_layer.cuh"
 
 namespace kda {

@@ -12,6 +12,12 @@
 // once per token (fp64 product and reduction to one turn, then fp32 sincospi)
 // and read from shared memory by all heads, a tile ahead; the next rows are in
 // flight while a step's are worked on.
+//
+// Measured on a B200 (6455 GB/s copy): unit rows of 16,384 tokens x 64 heads x
+// 128, bf16, 90 us = 6.0 TB/s (166 us with a block per token and nothing in
+// flight between its rows); 8192 tokens x 40 heads with half of each row turned
+// 47 us (the instructions of the turn and the weights, 74 % of the issue slots)
+// and its gradients 79 us = 5.3 TB/s.
 #include <math.h>
 
 #include "kda_layer.cuh"

@@ -20,6 +20,17 @@
 // memory that only the copying thread reads (cp.async, no registers); each
 // thread then turns its own into the fp32 rows that the scan reads, token by
 // token.
+//
+// Measured on a B200, bf16, 16 states: 32,768 tokens x 2048 channels in 797 us
+// (18 segments: 357 us for their own end states at 78 % of the special-function
+// unit, 460 us for the outputs at 68 % of it and 59 % of the issue slots; both
+// kernels take as long as their exponentials and their shared-memory words one
+// after the other, which is why twice the warps a scheduler gained nothing);
+// 12,001 packed tokens x 4096 in 400 us.  One token of 256 sequences x 4096: 32
+// us = 4.4 TB/s.  Tried and not kept: one state a thread (863 us for the long
+// prompt's outputs: its loads), a quarter of the exponentials as polynomials on
+// the multiply-add units (472 us instead of 460), tiles of 16 tokens and five or
+// six CTAs an SM (462 us).
 #include <math.h>
 
 #include "kda_scan.cuh"
