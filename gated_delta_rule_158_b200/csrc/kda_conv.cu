@@ -10,10 +10,11 @@
 // strip that crosses a sequence boundary starts a new run there.
 //
 // Measured on a B200 (6455 GB/s copy): 65,000 packed tokens x 4096 bf16 with
-// SiLU, 194 us = 5.5 TB/s; with rows prefetched to registers instead of the
-// ring it was 230 us, and one product per instruction instead of two (f32x2)
-// made the special-function and issue slots the bound (507 us at eight channels
-// a thread).  One token of 256 sequences x 12,288: 11.2 us, 4.5 TB/s.
+// SiLU, 194 us = 5.5 TB/s.  Before the ring, with loads as they were needed, it
+// took 507 us at eight channels a thread and 231 us at four; with the next rows
+// prefetched to registers 239 us; with the ring 213 us, and 193 us once the
+// strips filled whole waves.  One token of 256 sequences x 12,288: 11.2 us, 4.5
+// TB/s.
 // Gradients of 16,384 x 4096 (x bf16; dout, dx fp32): 114 us = 5.9 TB/s.
 #include "kda_layer.cuh"
 
@@ -26,59 +27,17 @@ constexpr int kRing = 16;    // rows of a thread's ring
 constexpr int kFV = 4;       // channels per thread of the step kernel
 
 // ------------------------------------------------------------ packed batch
-__global__ void seqlens_plan_kernel(const int32_t* __restrict__ cu, int N, int T,
-                                    StatusBlock* sb, int seg_len,
-                                    int32_t* __restrict__ seg_off) {
-  __shared__ int bad, carry;
-  __shared__ int wsum[32];
-  const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
-  if (tid == 0) {
-    bad = (cu[0] != 0 || cu[N] != T) ? 1 : 0;
-    carry = 0;
-  }
-  __syncthreads();
-  for (int n = tid; n < N; n += blockDim.x)
-    if (cu[n + 1] < cu[n]) atomicOr(&bad, 1);
-  __syncthreads();
-  if (tid == 0) {
+// The status word: KDA_OK or KDA_ERR_BAD_SEQLENS.
+__global__ void __launch_bounds__(1024) seqlens_plan_kernel(const int32_t* __restrict__ cu, int N,
+                                                            int T, StatusBlock* sb) {
+  int bad = threadIdx.x == 0 && (cu[0] != 0 || cu[N] != T);
+  for (int n = threadIdx.x; n < N; n += 1024) bad |= cu[n + 1] < cu[n];
+  bad = __syncthreads_or(bad);
+  if (threadIdx.x == 0) {
     sb->status = bad ? KDA_ERR_BAD_SEQLENS : KDA_OK;
     sb->detail = 0;
     sb->never_set = 0;
     sb->seqlens_ok = bad ? 0 : 1;
-  }
-  if (bad || seg_off == nullptr) return;
-  // exclusive prefix sums of the segment counts, blockDim.x sequences a step
-  for (int n0 = 0; n0 < N; n0 += blockDim.x) {
-    const int n = n0 + tid;
-    int c = 0;
-    if (n < N) {
-      const int len = cu[n + 1] - cu[n];
-      c = len > 0 ? 1 + (len - 1) / seg_len : 1;
-    }
-    int s = c;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int v = __shfl_up_sync(0xffffffffu, s, o);
-      if (lane >= o) s += v;
-    }
-    if (lane == 31) wsum[wid] = s;
-    __syncthreads();
-    if (wid == 0) {
-      int v = wsum[lane];
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int u = __shfl_up_sync(0xffffffffu, v, o);
-        if (lane >= o) v += u;
-      }
-      wsum[lane] = v;
-    }
-    __syncthreads();
-    const int before = carry + (wid ? wsum[wid - 1] : 0) + s - c;
-    if (n < N) seg_off[n] = before;
-    if (n == N - 1) seg_off[N] = before + c;
-    __syncthreads();
-    if (tid == 0) carry += wsum[31];
-    __syncthreads();
   }
 }
 
@@ -652,7 +611,11 @@ cudaError_t launch_step(const ConvArgs& a, void* state, int N, cudaStream_t st) 
   Tin* sp = static_cast<Tin*>(state);
   constexpr int NS = 4;
   const int64_t few = ((int64_t)N + NS - 1) / NS * CG;  // threads with four sequences each
-  if (few >= 148 * 512) {
+  // From 256 such threads an SM on; one sequence a thread against four, W = 4,
+  // bf16: 2.4 and 3.1 us at 55 threads an SM (32 sequences x 4096), 3.2 both at
+  // 166, 5.9 and 5.3 at 332, 6.7 and 5.1 at 443, 15.0 and 11.5 at 1328 (256 x
+  // 12,288).
+  if (few >= 148 * 256) {
     conv_step_kernel<Tin, W, NS>
         <<<(unsigned)((few + kConvThreads - 1) / kConvThreads), kConvThreads, 0, st>>>(a, sp, N);
   } else {
@@ -699,14 +662,12 @@ kda_status check_conv(kda_dtype dt, int D, int W, kda_activation act, int64_t x_
 // the launch grids are 32-bit
 bool grid_fits(int64_t items) { return items / kConvThreads < 0x7ffffff0LL / 2; }
 
-}  // namespace
-
-cudaError_t launch_seqlens_plan(const int32_t* cu, int N, int T, StatusBlock* sb, int seg_len,
-                                int32_t* seg_off, cudaStream_t stream) {
-  seqlens_plan_kernel<<<1, 1024, 0, stream>>>(cu, N, T, sb, seg_len, seg_off);
+cudaError_t launch_plan(const ConvArgs& a, cudaStream_t stream) {
+  seqlens_plan_kernel<<<1, 1024, 0, stream>>>(a.cu, a.num_seqs, a.T, a.sb);
   return cudaGetLastError();
 }
 
+}  // namespace
 }  // namespace kda
 
 using namespace kda;
@@ -755,7 +716,7 @@ kda_status kda_short_conv_fwd(const void* x, int64_t x_stride, const float* weig
     return KDA_ERR_UNSUPPORTED;
   cudaStream_t st = (cudaStream_t)stream;
   if (cu_seqlens)
-    if (cudaError_t e = launch_seqlens_plan(cu_seqlens, num_seqs, T, a.sb, 1, nullptr, st))
+    if (cudaError_t e = launch_plan(a, st))
       return cuda_failure(e);
   const cudaError_t e = in_dtype == KDA_BF16 ? dispatch_fwd<__nv_bfloat16>(a, W, st)
                                              : dispatch_fwd<float>(a, W, st);
@@ -852,7 +813,7 @@ kda_status kda_short_conv_bwd(const void* x, int64_t x_stride, const float* weig
     return KDA_ERR_UNSUPPORTED;
   cudaStream_t st = (cudaStream_t)stream;
   if (cu_seqlens)
-    if (cudaError_t e = launch_seqlens_plan(cu_seqlens, num_seqs, T, a.sb, 1, nullptr, st))
+    if (cudaError_t e = launch_plan(a, st))
       return cuda_failure(e);
   cudaError_t e = in_dtype == KDA_BF16 ? dispatch_bwd<__nv_bfloat16>(a, W, st)
                                        : dispatch_bwd<float>(a, W, st);

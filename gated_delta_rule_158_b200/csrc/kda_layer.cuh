@@ -63,12 +63,6 @@ inline kda_status check_batch(const int32_t* cu, int num_seqs, int B, int T) {
   return KDA_OK;
 }
 
-// Writes the status word (OK or KDA_ERR_BAD_SEQLENS) and, where seg_off is
-// not null, seg_off[n] = number of segments of seg_len tokens in the sequences
-// before n (a sequence has at least one segment; seg_off[N] is their total).
-cudaError_t launch_seqlens_plan(const int32_t* cu, int N, int T, StatusBlock* sb, int seg_len,
-                                int32_t* seg_off, cudaStream_t stream);
-
 // ---------------------------------------------------------- device helpers
 // The last n in [0, N) with off[n] <= i, for off non-decreasing from 0 and
 // i < off[N]: of empty ranges at i it skips all, so off[n] <= i < off[n + 1].
@@ -182,8 +176,8 @@ __device__ __forceinline__ float ex2(float x) {
 }
 
 // 1 / (1 + e^-x): e^-x = inf gives 0, NaN stays NaN.  The exponential is off by
-// (2 + |x|) 2^-22 of itself at most and the reciprocal by 2^-23, which a bf16
-// rounding (2^-9) hides; where |x| is large the result is 0 or 1 anyway.
+// (2 + |x|) 2^-22 of itself at most and the reciprocal by 2^-23: below 2^-19 of
+// the result for |x| <= 6, and a bf16 rounding is up to 2^-8.
 __device__ __forceinline__ float sigmoid_fast(float x) {
   float y;
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(1.0f + ex2(-kLog2e * x)));

@@ -14,8 +14,8 @@
 // flight while a step's are worked on.
 //
 // Measured on a B200 (6455 GB/s copy): unit rows of 16,384 tokens x 64 heads x
-// 128, bf16, 90 us = 6.0 TB/s (166 us with a block per token and nothing in
-// flight between its rows); 8192 tokens x 40 heads with half of each row turned
+// 128, bf16, 90 us = 6.0 TB/s (130 us before the blocks stayed and kept rows in
+// flight, 103 us before a group kept to its heads); 8192 tokens x 40 heads with half of each row turned
 // 47 us (the instructions of the turn and the weights, 74 % of the issue slots)
 // and its gradients 79 us = 5.3 TB/s.
 #include <math.h>
@@ -539,7 +539,6 @@ NormArgs norm_args(const void* q, int64_t q_stride, const void* k, int64_t k_str
   a.c = norm == KDA_NORM_RMS ? 1.0f / (float)d : 1.0f;
   a.eps = eps;
   a.pairs = rotation == KDA_ROT_PAIRS;
-
   return a;
 }
 

@@ -25,12 +25,12 @@
 // (18 segments: 357 us for their own end states at 78 % of the special-function
 // unit, 460 us for the outputs at 68 % of it and 59 % of the issue slots; both
 // kernels take as long as their exponentials and their shared-memory words one
-// after the other, which is why twice the warps a scheduler gained nothing);
+// after the other, and more warps a scheduler gained nothing);
 // 12,001 packed tokens x 4096 in 400 us.  One token of 256 sequences x 4096: 32
-// us = 4.4 TB/s.  Tried and not kept: one state a thread (863 us for the long
+// us = 4.4 TB/s.  Tried and not kept: one state a thread (878 us for the long
 // prompt's outputs: its loads), a quarter of the exponentials as polynomials on
-// the multiply-add units (472 us instead of 460), tiles of 16 tokens and five or
-// six CTAs an SM (462 us).
+// the multiply-add units (472 us instead of 460), tiles of 16 tokens (481 us), five
+// or six CTAs an SM (462 us).
 #include <math.h>
 
 #include "kda_scan.cuh"
@@ -96,6 +96,8 @@ __global__ void __launch_bounds__(Layout<S, SC_>::NT) scan_fwd_kernel(const Args
   const int nblk = a.G * ((a.D / a.G + CT - 1) / CT);
   const int ub = blockIdx.x / nblk;
   const Unit un = resolve(a.seg, a.sb, ub);
+  // of a packed batch's gradients kEnds runs the cut ones and kEnd the others
+  if (MODE != kOut && a.g_seg && a.seg.cu && un.valid && un.cut != (MODE == kEnds)) return;
   // a sequence's last segment has no successor that needs its end state, its
   // first none in front that needs its gradient; the checkpoints all do
   if (!un.valid || (MODE != kOut && !a.ckpt && un.last && (MODE == kEnd || un.first))) return;
@@ -109,8 +111,8 @@ __global__ void __launch_bounds__(Layout<S, SC_>::NT) scan_fwd_kernel(const Args
   float A2[SC][4];
   f2 h[SC][2], prod[SC][2], gs[SC][2];
   {
-    const float* from = MODE == kOut && a.h_seg ? a.h_seg + un.slot * ds
-                        : a.init && !(MODE != kOut && a.split) ? a.init + un.n * ds : nullptr;
+    const float* from = MODE == kOut && un.cut ? a.h_seg + un.slot * ds
+                        : a.init && !un.cut    ? a.init + un.n * ds : nullptr;
 #pragma unroll
     for (int q = 0; q < SC; ++q) {
 #pragma unroll
@@ -283,7 +285,7 @@ __global__ void __launch_bounds__(Layout<S, SC_>::NT) scan_fwd_kernel(const Args
 #pragma unroll
       for (int q = 0; q < SC; ++q) {
         store_pairs<2>(a.ckpt + at * ds + so + q * S, h[q]);
-        if (a.split && nl == 0) a.ckpt_dt[at * a.D + d + q] = cum[q];
+        if (un.cut && nl == 0) a.ckpt_dt[at * a.D + d + q] = cum[q];
       }
     }
   };
@@ -342,7 +344,7 @@ __global__ void __launch_bounds__(Layout<S, SC_>::NT) scan_fwd_kernel(const Args
     if (MODE == kOut) store_tile(i);
   }
   if (MODE != kOut) {
-    if (!a.split) return;  // the checkpoints alone were wanted
+    if (!un.cut) return;  // the checkpoints alone were wanted
     if (live) {
 #pragma unroll
       for (int q = 0; q < SC; ++q) {
@@ -374,7 +376,8 @@ __global__ void __launch_bounds__(Layout<S, SC_>::NT) scan_fwd_kernel(const Args
 // with g_seg the state gradients from the right likewise: g_in[last] = d_final,
 // g_in[k-1] = e^{A sum dt_k} g_in[k] + g_k.
 __global__ void __launch_bounds__(256) scan_combine_kernel(const Args a) {
-  if (a.seg.cu && !a.sb->seqlens_ok) return;
+  // a batch that was not cut uses neither h_seg nor g_seg
+  if (a.seg.cu && (!a.sb->seqlens_ok || a.sb->pad[0] >= a.seg.T)) return;
   const int64_t per = (int64_t)a.D * a.S / 4;
   const int64_t idx = (int64_t)blockIdx.x * 256 + threadIdx.x;
   const int n = (int)(idx / per);
@@ -507,13 +510,14 @@ __global__ void __launch_bounds__(256) scan_step_kernel(const Args a, float* sta
   }
 }
 
-// Packed batches: validates the offsets, then chooses the segment length (a.seg
-// .seg_len where a sequence is longer than that, else the whole batch's
+// Packed batches: validates the offsets, then chooses the segment length
+// (seg_len where a sequence is longer than cut_above, else the whole batch's
 // length, so that every sequence is one unit) and writes seg_off and order.
 constexpr int kMaxOrder = 2048;
 
 __global__ void __launch_bounds__(1024) scan_plan_kernel(const int32_t* __restrict__ cu, int N,
-                                                         int T, StatusBlock* sb, int seg_len,
+                                                         int T, StatusBlock* sb, int cut_above,
+                                                         int seg_len,
                                                          int32_t* __restrict__ seg_off,
                                                          int32_t* __restrict__ order) {
   __shared__ int bad, longest, carry;
@@ -539,10 +543,10 @@ __global__ void __launch_bounds__(1024) scan_plan_kernel(const int32_t* __restri
     sb->detail = 0;
     sb->never_set = 0;
     sb->seqlens_ok = bad ? 0 : 1;
-    sb->pad[0] = longest > seg_len ? seg_len : T;
+    sb->pad[0] = longest > cut_above ? seg_len : T;
   }
   if (bad) return;
-  const int sl = longest > seg_len ? seg_len : T;
+  const int sl = longest > cut_above ? seg_len : T;
   // longest first; batches of more sequences keep their order
   for (int n = tid; n < N; n += 1024) {
     int rank = n;
@@ -604,21 +608,23 @@ cudaError_t launch_one(const Args& a, cudaStream_t st) {
 
 template <typename Tin, int MODE>
 cudaError_t launch_mode(const Args& a, cudaStream_t st) {
-  if (a.seg.wide) {
-    switch (a.S) {
-      case 8: return launch_one<Tin, 8, 1, MODE>(a, st);  // the lanes of a channel pair are few
-      case 16: return launch_one<Tin, 16, 2, MODE>(a, st);
-      case 32: return launch_one<Tin, 32, 2, MODE>(a, st);
-      case 64: return launch_one<Tin, 64, 2, MODE>(a, st);
-      default: return launch_one<Tin, 128, 2, MODE>(a, st);
+  if constexpr (MODE == kOut) {  // the other modes' batches fill the GPU with pairs
+    if (!a.seg.wide) {
+      switch (a.S) {
+        case 8: return launch_one<Tin, 8, 1, MODE>(a, st);
+        case 16: return launch_one<Tin, 16, 1, MODE>(a, st);
+        case 32: return launch_one<Tin, 32, 1, MODE>(a, st);
+        case 64: return launch_one<Tin, 64, 1, MODE>(a, st);
+        default: return launch_one<Tin, 128, 1, MODE>(a, st);
+      }
     }
   }
   switch (a.S) {
-    case 8: return launch_one<Tin, 8, 1, MODE>(a, st);
-    case 16: return launch_one<Tin, 16, 1, MODE>(a, st);
-    case 32: return launch_one<Tin, 32, 1, MODE>(a, st);
-    case 64: return launch_one<Tin, 64, 1, MODE>(a, st);
-    default: return launch_one<Tin, 128, 1, MODE>(a, st);
+    case 8: return launch_one<Tin, 8, 1, MODE>(a, st);  // the lanes of a channel pair are few
+    case 16: return launch_one<Tin, 16, 2, MODE>(a, st);
+    case 32: return launch_one<Tin, 32, 2, MODE>(a, st);
+    case 64: return launch_one<Tin, 64, 2, MODE>(a, st);
+    default: return launch_one<Tin, 128, 2, MODE>(a, st);
   }
 }
 
@@ -632,8 +638,12 @@ template <typename Tin, int S>
 cudaError_t launch_step_s(const Args& a, float* state, int N, cudaStream_t st) {
   if constexpr (S >= 16) {
     constexpr int NSEQ = 4;
+    // threads with four sequences each
     const int64_t many = ((int64_t)N + NSEQ - 1) / NSEQ * a.D * (S / 4);
-    if (many >= 148 * 1024) {  // every SM has 1024 threads with four sequences each
+    // From 512 such threads an SM on; one sequence a thread against four, D =
+    // 4096, S = 16, bf16: 3.1 and 3.2 us at 221 threads an SM (8 sequences), 7.4
+    // and 6.4 at 886, 12.3 and 10.7 at 1771, 42.0 and 32.8 at 7085 (256).
+    if (many >= 148 * 512) {
       scan_step_kernel<Tin, S, NSEQ><<<(unsigned)((many + 255) / 256), 256, 0, st>>>(a, state, N);
       return cudaGetLastError();
     }
@@ -657,14 +667,16 @@ cudaError_t launch_step(const Args& a, float* state, int N, cudaStream_t st) {
 }  // namespace
 
 cudaError_t launch_scan_plan(const Args& a, int32_t* seg_off, int32_t* order, cudaStream_t st) {
-  scan_plan_kernel<<<1, 1024, 0, st>>>(a.seg.cu, a.seg.num_seqs, a.seg.T, a.sb, a.seg.seg_len,
-                                       seg_off, order);
+  scan_plan_kernel<<<1, 1024, 0, st>>>(a.seg.cu, a.seg.num_seqs, a.seg.T, a.sb, a.seg.cut_above,
+                                       a.seg.seg_len, seg_off, order);
   return cudaGetLastError();
 }
 
 cudaError_t launch_ends(const Args& a, kda_dtype dt, cudaStream_t st) {
-  if (cudaError_t e = a.g_seg ? launch_typed<kEnds>(a, dt, st) : launch_typed<kEnd>(a, dt, st))
-    return e;
+  if (!a.g_seg || a.seg.cu)
+    if (cudaError_t e = launch_typed<kEnd>(a, dt, st)) return e;
+  if (a.g_seg)
+    if (cudaError_t e = launch_typed<kEnds>(a, dt, st)) return e;
   if (!a.split) return cudaSuccess;
   const int64_t items = (int64_t)a.seg.num_seqs * a.D * a.S / 4;
   scan_combine_kernel<<<(unsigned)((items + 255) / 256), 256, 0, st>>>(a);
@@ -677,16 +689,25 @@ bool sizes_ok(int D, int S, int G) {
 }
 
 // How a batch is spread over the GPU.  `warps` is its sequences' warps with two
-// channels a thread; 592 schedulers want two to four each.  Dense batches:
-//   from 8 a scheduler's four warps on (SMs x 8): two channels a thread;
-//   from SMs x 3: one channel a thread, twice the warps;
+// channels a thread.  Dense batches (us for two channels a thread, one channel,
+// and cut; S = 16, T = 2048, D = 2048, that is 128 warps a sequence):
+//   from SMs x 6: two channels a thread (289, 324, 406 at 6.9 warps an SM;
+//     388, 395, 514 at 8.6);
+//   from SMs x 3: one channel a thread, twice the warps (207, 200, 229 at 3.5;
+//     289, 258, 311 at 5.2);
 //   fewer: the sequences are cut until there are SMs x 16 warps, which costs
-//   a second pass over all but the last segments.
-// Packed batches do not show their lengths to the host: one channel a thread
-// unless there are many sequences, and a cut (the plan kernel's choice) only
-// where a sequence is longer than the time that the whole batch takes.  The
-// gradients' walk has two warps a scheduler at most (its registers) and wants
-// both; its first pass over the segments is needed anyway.
+//     a second pass over all but the last segments (200, 144, 66 at 0.9; 205,
+//     199, 159 at 2.6).
+// The gradients' first pass over the segments is needed anyway and their walk
+// has two warps a scheduler at most: cut until there are SMs x 32 warps, four
+// waves (493 us; 555 with SMs x 8 or 16 at 3.5 warps an SM).
+// Packed batches do not show their lengths to the host: two channels a thread,
+// and a cut (the plan kernel's choice) into halves of the even share of SMs x
+// 16 warps, where one sequence is longer than three shares.  12,000 tokens x
+// 4096 x 16 in 16 sequences, the longest of 2.3, 3.1, 4.6, 6.9 shares: uncut
+// 401, 491, 669, 930 us; cut at half a share 442, 442, 461, 508 (at one share
+// 475, 479, 523, 591; at four 409, 499, 953, 1002); gradients uncut 1269, 1532,
+// 2084, 2906, cut at half a share 1442, 1457, 1410, 1363.
 Segments plan_segments(const int32_t* cu, int num_seqs, int B, int T, int D, int S, bool bwd) {
   constexpr int64_t kSms = 148;
   Segments m{};
@@ -698,10 +719,14 @@ Segments plan_segments(const int32_t* cu, int num_seqs, int B, int T, int D, int
   int64_t len = T;
   if (cu) {
     m.wide = true;
-    len = 4 * T * per_seq / (kSms * 16);
-    if (len < 256) len = 256;
+    len = T * per_seq / (kSms * 32);
+    if (len < 64) len = 64;
+    len = (len + kTile - 1) / kTile * kTile;
+    const int64_t above = 6 * len < 512 ? 512 : 6 * len;  // shorter: the extra launches
+    m.cut_above = (int)(above < T ? above : T);
+    if (m.cut_above == T) len = T;
   } else {
-    m.wide = warps >= kSms * 8;
+    m.wide = warps >= kSms * 6;
     if (warps < kSms * (bwd ? 32 : 3)) {
       int64_t segs = kSms * (bwd ? 32 : 16) / warps;
       if (segs > T / 64) segs = T / 64;
@@ -710,8 +735,8 @@ Segments plan_segments(const int32_t* cu, int num_seqs, int B, int T, int D, int
         len = (T + segs - 1) / segs;
       }
     }
+    len = (len + kTile - 1) / kTile * kTile;
   }
-  len = (len + kTile - 1) / kTile * kTile;
   m.seg_len = (int)(len < T ? len : T);
   m.segs = (T + m.seg_len - 1) / m.seg_len;
   m.units = cu ? num_seqs + T / m.seg_len : B * m.segs;
@@ -777,10 +802,6 @@ size_t kda_selective_scan_fwd_workspace_size(int B, int T, int D, int S, int G, 
          align256(sizeof(float) * (size_t)m.units * D);
   return b;
 }
-
-}  // extern "C"
-
-extern "C" {
 
 kda_status kda_selective_scan_fwd(const void* x, int64_t x_stride, const void* delta,
                                   int64_t delta_stride, const float* A, const void* Bm,

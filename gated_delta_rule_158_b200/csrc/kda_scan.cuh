@@ -17,7 +17,8 @@ struct Segments {
   const int32_t* seg_off;  // packed
   const int32_t* order;    // packed
   int num_seqs, T, seg_len, segs, units;
-  bool wide;               // forward: two channels a thread
+  int cut_above;           // packed: only a batch with a longer sequence is cut
+  bool wide;               // the outputs' kernel: two channels a thread
 };
 
 struct Unit {
@@ -25,6 +26,7 @@ struct Unit {
   int slot;          // index of the segment's states, in token order
   int64_t t0, t1;    // its tokens
   bool first, last;  // of its sequence
+  bool cut;          // the batch has sequences of several segments
   bool valid;
 };
 
@@ -54,6 +56,7 @@ __device__ __forceinline__ Unit resolve(const Segments& m, StatusBlock* sb, int 
     end = start + m.T;
   }
   u.first = k == 0;
+  u.cut = m.cu ? len < m.T : m.segs > 1;
   u.t0 = start + (int64_t)k * len;
   u.t1 = u.last ? end : u.t0 + len;
   if (m.cu)
@@ -79,7 +82,7 @@ struct Args {
   void* out;
   int D, S, G;
   Segments seg;
-  bool split;     // some sequence may have more than one segment
+  bool split;     // some sequence may have more than one segment (Unit::cut: has)
   float* h_seg;   // [units][D][S]: a segment's end state from zero, then its incoming state
   float* dt_sum;  // [units][D]: the segment's sum of dt
   StatusBlock* sb;

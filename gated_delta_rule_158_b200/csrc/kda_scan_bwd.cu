@@ -183,12 +183,12 @@ __global__ void __launch_bounds__(Walk<S>::NT, Walk<S>::kCtas) scan_bwd_kernel(c
 #pragma unroll
     for (int i = 0; i < 2; ++i) A2[q][i] = carry[q][i] = dA[q][i] = dA_err[q][i] = zero2();
   if (live) {
-    const float* from = a.split ? a.g_seg + un.slot * ds : a.d_final ? a.d_final + un.n * ds : nullptr;
+    const float* from = un.cut ? a.g_seg + un.slot * ds : a.d_final ? a.d_final + un.n * ds : nullptr;
 #pragma unroll
     for (int q = 0; q < 2; ++q) {
       load_pairs<2>(a.A + so + q * S, A2[q]);
       if (from) load_pairs<2>(from + so + q * S, carry[q]);
-      if (a.split) {
+      if (un.cut) {
         f2 hin[2];
         load_pairs<2>(a.h_seg + un.slot * ds + so + q * S, hin);
         store_pairs<2>(own_hin + q * 4 * NT, hin);
@@ -301,7 +301,7 @@ __global__ void __launch_bounds__(Walk<S>::NT, Walk<S>::kCtas) scan_bwd_kernel(c
     for (int q = 0; q < 2; ++q) {
       copy_in<16>(reinterpret_cast<char*>(keep_at(step, q)),
                   in ? a.ckpt + (tile0 + step) * ds + so + q * S : a.ckpt, in);
-      if (a.split)
+      if (un.cut)
         copy_in<4>(reinterpret_cast<char*>(keep_dt_at(step, q)),
                    in ? a.ckpt_dt + (tile0 + step) * a.D + d + q : a.ckpt_dt, in);
     }
@@ -317,7 +317,7 @@ __global__ void __launch_bounds__(Walk<S>::NT, Walk<S>::kCtas) scan_bwd_kernel(c
 #pragma unroll
     for (int q = 0; q < 2; ++q) {
       load_pairs<2>(keep_at(step, q), h0[q]);
-      if (a.split && live) {
+      if (un.cut && live) {
         const float past = *keep_dt_at(step, q);
         f2 hin[2];
         load_pairs<2>(own_hin + q * 4 * NT, hin);

@@ -304,3 +304,51 @@ def test_two_streams_at_once():
     for k, pair in enumerate(both):
         for a, b in zip(pair, alone[k % 2]):
             assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("spread", [
+    # a packed batch is cut only where a sequence has more than 512 tokens (with
+    # few channels): the longest just at the limit, just beyond it, and beyond it
+    # in the last and in a single sequence
+    (1, 1200, 32, 16, 2, [0, 512, 600, 600, 1112, 1200]),
+    (1, 1200, 32, 16, 2, [0, 513, 600, 600, 1112, 1200]),
+    (1, 1200, 40, 8, 1, [0, 1, 65, 130, 1200]),
+    (1, 545, 264, 128, 1, [0, 545]),
+    (1, 512, 264, 32, 1, [0, 512]),
+])
+def test_packed_batches_around_the_cut(spread):
+    test_scan_spreads(spread)
+
+
+@pytest.mark.parametrize("kind", ["conv", "scan"])
+def test_steps_of_many_sequences(kind):
+    """Steps on both sides of the size from which a thread takes four sequences,
+    with and without a remainder: bit-identical to the sequences one by one."""
+    gen = torch.Generator().manual_seed(3)
+    for N in (1, 31, 45, 122):
+        if kind == "conv":
+            D, Wd = 5000, 4
+            x, w, b = draw(gen, N, D, dtype=BF16), draw(gen, D, Wd, scale=0.5), draw(gen, D)
+            state = draw(gen, N, Wd - 1, D, dtype=BF16)
+            one, out, ref = state.clone(), torch.empty_like(x), torch.empty_like(x)
+            kda.kda_short_conv_step(x, w, state, out, bias=b)
+            for n in range(N):
+                kda.kda_short_conv_step(x[n:n + 1], w, one[n:n + 1], ref[n:n + 1], bias=b)
+        else:
+            D, S = 1504, 32
+            x, delta, z = (draw(gen, N, D, dtype=BF16) for _ in range(3))
+            A = -torch.rand(D, S, generator=gen).to(DEV) * S
+            Bm, Cm = (draw(gen, N, 1, S, dtype=BF16) for _ in range(2))
+            state = draw(gen, N, D, S)
+            one, out, ref = state.clone(), torch.empty_like(x), torch.empty_like(x)
+            kda.kda_selective_scan_step(x, delta, A, Bm, Cm, state, out, z=z)
+            for n in range(N):
+                k = slice(n, n + 1)
+                kda.kda_selective_scan_step(x[k], delta[k], A, Bm[k], Cm[k], one[k], ref[k],
+                                            z=z[k])
+        assert torch.equal(state, one)
+        # the scan's outputs are summed over a channel's lanes in another order
+        if kind == "conv":
+            assert torch.equal(out, ref)
+        else:
+            near(out, host(ref), BF16)
