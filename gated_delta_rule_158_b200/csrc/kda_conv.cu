@@ -10,7 +10,7 @@
 // strip that crosses a sequence boundary starts a new run there.
 //
 // Measured on a B200 (6455 GB/s copy): 65,000 packed tokens x 4096 bf16 with
-// SiLU, 194 us = 5.5 TB/s.  Before the ring, with loads as they were needed, it
+// SiLU, 193 to 207 us = 5.2 to 5.5 TB/s.  Before the ring, with loads as they were needed, it
 // took 507 us at eight channels a thread and 231 us at four; with the next rows
 // prefetched to registers 239 us; with the ring 213 us, and 193 us once the
 // strips filled whole waves.  One token of 256 sequences x 12,288: 11.2 us, 4.5
@@ -416,7 +416,8 @@ __global__ void __launch_bounds__(kConvThreads, 2) conv_bwd_kernel(const ConvArg
 #pragma unroll
     for (int i = 0; i < P; ++i) {  // silu'(p) = s + p s (1 - s)
       const f2 s = sigmoid2(p[i]), ps = mul2(p[i], s);
-      dss[u + W - 1][i] = mul2(dss[u + W - 1][i], fma2(ps, fma2(s, pack2(-1.f, -1.f), pack2(1.f, 1.f)), s));
+      dss[u + W - 1][i] = mul2(
+          dss[u + W - 1][i], fma2(ps, fma2(s, pack2(-1.f, -1.f), pack2(1.f, 1.f)), s));
     }
   };
   auto sums_of = [&](int u) {

@@ -109,11 +109,6 @@ __device__ __forceinline__ float2 bf2_to_f2(uint32_t u) {
 }
 
 template <>
-__device__ __forceinline__ void load_vec<__nv_bfloat16, 1>(const __nv_bfloat16* p,
-                                                           float (&v)[1]) {
-  v[0] = __bfloat162float(*p);
-}
-template <>
 __device__ __forceinline__ void load_vec<__nv_bfloat16, 2>(const __nv_bfloat16* p,
                                                            float (&v)[2]) {
   const float2 a = bf2_to_f2(*(reinterpret_cast<const uint32_t*>(p)));
@@ -142,9 +137,7 @@ __device__ __forceinline__ uint32_t f2_to_bf2(float a, float b) {
 
 template <int V>
 __device__ __forceinline__ void store_vec(float* p, const float (&v)[V]) {
-  if constexpr (V == 1) {
-    *p = v[0];
-  } else if constexpr (V == 2) {
+  if constexpr (V == 2) {
     *reinterpret_cast<float2*>(p) = make_float2(v[0], v[1]);
   } else {
 #pragma unroll
@@ -154,9 +147,7 @@ __device__ __forceinline__ void store_vec(float* p, const float (&v)[V]) {
 }
 template <int V>
 __device__ __forceinline__ void store_vec(__nv_bfloat16* p, const float (&v)[V]) {
-  if constexpr (V == 1) {
-    *p = __float2bfloat16_rn(v[0]);
-  } else if constexpr (V == 2) {
+  if constexpr (V == 2) {
     *reinterpret_cast<uint32_t*>(p) = f2_to_bf2(v[0], v[1]);
   } else if constexpr (V == 4) {
     *reinterpret_cast<uint2*>(p) = make_uint2(f2_to_bf2(v[0], v[1]), f2_to_bf2(v[2], v[3]));
@@ -221,21 +212,14 @@ __device__ __forceinline__ float sum2(f2 v) {
 }
 __device__ __forceinline__ f2 zero2() { return 0ull; }
 
-// 2 N consecutive floats as N pairs (aligned to their size)
-template <int N>
-__device__ __forceinline__ void load_pairs(const float* p, f2 (&v)[N]) {
-  if constexpr (N == 1) {
-    v[0] = *reinterpret_cast<const f2*>(p);
-  } else {
-    const ulonglong2 u = *reinterpret_cast<const ulonglong2*>(p);
-    v[0] = u.x;
-    v[1] = u.y;
-  }
+// four consecutive floats as two pairs (16-byte aligned)
+__device__ __forceinline__ void load_pairs(const float* p, f2 (&v)[2]) {
+  const ulonglong2 u = *reinterpret_cast<const ulonglong2*>(p);
+  v[0] = u.x;
+  v[1] = u.y;
 }
-template <int N>
-__device__ __forceinline__ void store_pairs(float* p, const f2 (&v)[N]) {
-  if constexpr (N == 1) *reinterpret_cast<f2*>(p) = v[0];
-  else *reinterpret_cast<ulonglong2*>(p) = make_ulonglong2(v[0], v[1]);
+__device__ __forceinline__ void store_pairs(float* p, const f2 (&v)[2]) {
+  *reinterpret_cast<ulonglong2*>(p) = make_ulonglong2(v[0], v[1]);
 }
 
 // sigmoid_fast of both
@@ -267,8 +251,12 @@ __device__ __forceinline__ void copy_in(char* to, const void* from, bool in) {
                    : "memory");
   }
 }
-__device__ __forceinline__ void copies_issued() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-__device__ __forceinline__ void copies_landed() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+__device__ __forceinline__ void copies_issued() {
+  asm volatile("cp.async.commit_group;" ::: "memory");
+}
+__device__ __forceinline__ void copies_landed() {
+  asm volatile("cp.async.wait_all;" ::: "memory");
+}
 
 // all but the latest N committed groups of copies have landed
 template <int N>
@@ -288,18 +276,15 @@ __device__ __forceinline__ void read_slot(const char* p, float (&v)[V]) {
 template <typename T, int V>
 struct Raw {
   static constexpr int BYTES = V * (int)sizeof(T);
-  static constexpr int N = BYTES < 4 ? 1 : BYTES / 4;
+  static constexpr int N = BYTES / 4;
+  static_assert(BYTES == 8 || BYTES % 16 == 0, "vector width");
   uint32_t r[N];
   __device__ __forceinline__ void zero() {
 #pragma unroll
     for (int i = 0; i < N; ++i) r[i] = 0;
   }
   __device__ __forceinline__ void load(const T* p) {
-    if constexpr (BYTES == 2) {
-      r[0] = *reinterpret_cast<const unsigned short*>(p);
-    } else if constexpr (BYTES == 4) {
-      r[0] = *reinterpret_cast<const uint32_t*>(p);
-    } else if constexpr (BYTES == 8) {
+    if constexpr (BYTES == 8) {
       const uint2 u = *reinterpret_cast<const uint2*>(p);
       r[0] = u.x; r[1] = u.y;
     } else {
@@ -311,11 +296,7 @@ struct Raw {
     }
   }
   __device__ __forceinline__ void store(T* p) const {
-    if constexpr (BYTES == 2) {
-      *reinterpret_cast<unsigned short*>(p) = (unsigned short)r[0];
-    } else if constexpr (BYTES == 4) {
-      *reinterpret_cast<uint32_t*>(p) = r[0];
-    } else if constexpr (BYTES == 8) {
+    if constexpr (BYTES == 8) {
       *reinterpret_cast<uint2*>(p) = make_uint2(r[0], r[1]);
     } else {
 #pragma unroll

@@ -15,9 +15,9 @@
 //
 // Measured on a B200 (6455 GB/s copy): unit rows of 16,384 tokens x 64 heads x
 // 128, bf16, 90 us = 6.0 TB/s (130 us before the blocks stayed and kept rows in
-// flight, 103 us before a group kept to its heads); 8192 tokens x 40 heads with half of each row turned
-// 47 us (the instructions of the turn and the weights, 74 % of the issue slots)
-// and its gradients 79 us = 5.3 TB/s.
+// flight, 103 us before a group kept to its heads); 8192 tokens x 40 heads with
+// half of each row turned 47 us (the instructions of the turn and the weights,
+// 74 % of the issue slots) and its gradients 79 us = 5.3 TB/s.
 #include <math.h>
 
 #include "kda_layer.cuh"
@@ -144,8 +144,8 @@ __device__ __forceinline__ void turn(const NormArgs& a, const float* tab, int to
   const float* at = tab + tok * a.rot + 4 * l;
   if constexpr (ROT == kHalves) {
     f2 c[2], s[2];
-    load_pairs<2>(at, c);
-    load_pairs<2>(at + (a.rot >> 1), s);
+    load_pairs(at, c);
+    load_pairs(at + (a.rot >> 1), s);
     const f2 one = pack2(sgn, sgn), neg = pack2(-sgn, -sgn);
 #pragma unroll
     for (int i = 0; i < 2; ++i) {

@@ -26,7 +26,7 @@
 // unit, 460 us for the outputs at 68 % of it and 59 % of the issue slots; both
 // kernels take as long as their exponentials and their shared-memory words one
 // after the other, and more warps a scheduler gained nothing);
-// 12,001 packed tokens x 4096 in 400 us.  One token of 256 sequences x 4096: 32
+// 12,001 packed tokens x 4096 in 400 to 420 us.  One token of 256 sequences x 4096: 32
 // us = 4.4 TB/s.  Tried and not kept: one state a thread (878 us for the long
 // prompt's outputs: its loads), a quarter of the exponentials as polynomials on
 // the multiply-add units (472 us instead of 460), tiles of 16 tokens (481 us), five
@@ -124,7 +124,7 @@ __global__ void __launch_bounds__(Layout<S, SC_>::NT) scan_fwd_kernel(const Args
       }
       if (live) {
         load_vec<float, 4>(a.A + so + q * S, A2[q]);
-        if (from) load_pairs<2>(from + so + q * S, h[q]);
+        if (from) load_pairs(from + so + q * S, h[q]);
       }
 #pragma unroll
       for (int i = 0; i < 4; ++i) A2[q][i] *= kLog2e;
@@ -245,8 +245,8 @@ __global__ void __launch_bounds__(Layout<S, SC_>::NT) scan_fwd_kernel(const Args
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
       load_du<SC>(pdu + (t + k) * M::kRow, g.dt[k], g.u[k]);
-      load_pairs<2>(pb + (t + k) * S, g.b[k]);
-      if (MODE != kEnd) load_pairs<2>(pc + (t + k) * S, g.c[k]);
+      load_pairs(pb + (t + k) * S, g.b[k]);
+      if (MODE != kEnd) load_pairs(pc + (t + k) * S, g.c[k]);
       if (MODE == kEnds) load_vec<float, SC>(pdy + (t + k) * CT, g.dy[k]);
     }
   };
@@ -284,7 +284,7 @@ __global__ void __launch_bounds__(Layout<S, SC_>::NT) scan_fwd_kernel(const Args
       const int64_t at = tile0 + t / kStep;
 #pragma unroll
       for (int q = 0; q < SC; ++q) {
-        store_pairs<2>(a.ckpt + at * ds + so + q * S, h[q]);
+        store_pairs(a.ckpt + at * ds + so + q * S, h[q]);
         if (un.cut && nl == 0) a.ckpt_dt[at * a.D + d + q] = cum[q];
       }
     }
@@ -348,8 +348,8 @@ __global__ void __launch_bounds__(Layout<S, SC_>::NT) scan_fwd_kernel(const Args
     if (live) {
 #pragma unroll
       for (int q = 0; q < SC; ++q) {
-        store_pairs<2>(a.h_seg + un.slot * ds + so + q * S, h[q]);
-        if (MODE == kEnds) store_pairs<2>(a.g_seg + un.slot * ds + so + q * S, gs[q]);
+        store_pairs(a.h_seg + un.slot * ds + so + q * S, h[q]);
+        if (MODE == kEnds) store_pairs(a.g_seg + un.slot * ds + so + q * S, gs[q]);
       }
     }
     // dt summed over the threads that share a channel group, in order
@@ -367,7 +367,7 @@ __global__ void __launch_bounds__(Layout<S, SC_>::NT) scan_fwd_kernel(const Args
     }
   } else if (un.last && a.final_state && live) {
 #pragma unroll
-    for (int q = 0; q < SC; ++q) store_pairs<2>(a.final_state + un.n * ds + so + q * S, h[q]);
+    for (int q = 0; q < SC; ++q) store_pairs(a.final_state + un.n * ds + so + q * S, h[q]);
   }
 }
 
@@ -460,7 +460,7 @@ __global__ void __launch_bounds__(256) scan_step_kernel(const Args a, float* sta
     b[k].zero();
     c[k].zero();
     if (k < ns) {
-      load_pairs<2>(state + (n0 + k) * ds + so, h[k]);
+      load_pairs(state + (n0 + k) * ds + so, h[k]);
       b[k].load(static_cast<const Tin*>(a.Bm) + (n0 + k) * a.B_stride + g * S + nl * 4);
       c[k].load(static_cast<const Tin*>(a.Cm) + (n0 + k) * a.C_stride + g * S + nl * 4);
     }
@@ -491,7 +491,7 @@ __global__ void __launch_bounds__(256) scan_step_kernel(const Args a, float* sta
     const f2 w1 = pack2(decay(sk, A2[2]), decay(sk, A2[3]));
     h[k][0] = fma2(w0, h[k][0], mul2(uu, pack2(b[k].at(0), b[k].at(1))));
     h[k][1] = fma2(w1, h[k][1], mul2(uu, pack2(b[k].at(2), b[k].at(3))));
-    if (k < ns) store_pairs<2>(state + (n0 + k) * ds + so, h[k]);
+    if (k < ns) store_pairs(state + (n0 + k) * ds + so, h[k]);
     y[k] = sum2(fma2(pack2(c[k].at(2), c[k].at(3)), h[k][1],
                      mul2(pack2(c[k].at(0), c[k].at(1)), h[k][0])));
   }
@@ -794,7 +794,8 @@ size_t kda_selective_scan_fwd_workspace_size(int B, int T, int D, int S, int G, 
       (int64_t)B * T > kMaxRows)
     return 0;
   static const int32_t packed = 0;  // only whether there are offsets matters here
-  const Segments m = plan_segments(num_seqs > 0 && B == 1 ? &packed : nullptr, num_seqs, B, T, D, S, false);
+  const Segments m = plan_segments(num_seqs > 0 && B == 1 ? &packed : nullptr, num_seqs, B, T,
+                                   D, S, false);
   size_t b = kStatusBytes;
   if (m.cu) b += 2 * align256(sizeof(int32_t) * ((size_t)num_seqs + 1));
   if (m.segs > 1)

@@ -18,7 +18,7 @@
 // partial sums of dB, dC (one per channel block), dA, dD and ddelta_bias (one
 // per segment) are added in a fixed order.  Nothing is added atomically.
 //
-// The walk is bound by its instructions (some 20 per state element and token)
+// The walk is bound by its instructions (24 per state element and token)
 // at the two warps per scheduler that its registers leave: a thread has 4
 // states of 2 channels, so that the sums over channels (dB, dC: 8 values a
 // token) and over states (3 per channel) are halved before they cross lanes,
@@ -183,15 +183,16 @@ __global__ void __launch_bounds__(Walk<S>::NT, Walk<S>::kCtas) scan_bwd_kernel(c
 #pragma unroll
     for (int i = 0; i < 2; ++i) A2[q][i] = carry[q][i] = dA[q][i] = dA_err[q][i] = zero2();
   if (live) {
-    const float* from = un.cut ? a.g_seg + un.slot * ds : a.d_final ? a.d_final + un.n * ds : nullptr;
+    const float* from = un.cut      ? a.g_seg + un.slot * ds
+                        : a.d_final ? a.d_final + un.n * ds : nullptr;
 #pragma unroll
     for (int q = 0; q < 2; ++q) {
-      load_pairs<2>(a.A + so + q * S, A2[q]);
-      if (from) load_pairs<2>(from + so + q * S, carry[q]);
+      load_pairs(a.A + so + q * S, A2[q]);
+      if (from) load_pairs(from + so + q * S, carry[q]);
       if (un.cut) {
         f2 hin[2];
-        load_pairs<2>(a.h_seg + un.slot * ds + so + q * S, hin);
-        store_pairs<2>(own_hin + q * 4 * NT, hin);
+        load_pairs(a.h_seg + un.slot * ds + so + q * S, hin);
+        store_pairs(own_hin + q * 4 * NT, hin);
       }
       A2[q][0] = mul2(A2[q][0], pack2(kLog2e, kLog2e));
       A2[q][1] = mul2(A2[q][1], pack2(kLog2e, kLog2e));
@@ -316,11 +317,11 @@ __global__ void __launch_bounds__(Walk<S>::NT, Walk<S>::kCtas) scan_bwd_kernel(c
     f2 h0[2][2], hs[kStep][2][2], dAs[2][2];
 #pragma unroll
     for (int q = 0; q < 2; ++q) {
-      load_pairs<2>(keep_at(step, q), h0[q]);
+      load_pairs(keep_at(step, q), h0[q]);
       if (un.cut && live) {
         const float past = *keep_dt_at(step, q);
         f2 hin[2];
-        load_pairs<2>(own_hin + q * 4 * NT, hin);
+        load_pairs(own_hin + q * 4 * NT, hin);
 #pragma unroll
         for (int k = 0; k < 2; ++k)
           h0[q][k] = fma2(ex2_2(mul2(pack2(past, past), A2[q][k])), hin[k], h0[q][k]);
@@ -332,7 +333,7 @@ __global__ void __launch_bounds__(Walk<S>::NT, Walk<S>::kCtas) scan_bwd_kernel(c
     for (int t = 0; t < kStep; ++t) {
       f2 b[2];
       float dt[2], u[2];
-      load_pairs<2>(pb + t * S, b);
+      load_pairs(pb + t * S, b);
       load_du<2>(pdu + t * L::kRow, dt, u);
 #pragma unroll
       for (int q = 0; q < 2; ++q) {
@@ -358,8 +359,8 @@ __global__ void __launch_bounds__(Walk<S>::NT, Walk<S>::kCtas) scan_bwd_kernel(c
         const int t = t4 + m;
         f2 b[2], cc[2], pB[2], pC[2];
         float dt[2], u[2], dys[2], gA[2], gB[2], yy[2];
-        load_pairs<2>(pb + t * S, b);
-        load_pairs<2>(pc + t * S, cc);
+        load_pairs(pb + t * S, b);
+        load_pairs(pc + t * S, cc);
         load_du<2>(pdu + t * L::kRow, dt, u);
         load_vec<float, 2>(pdy + t * CT, dys);
 #pragma unroll
@@ -499,8 +500,8 @@ __global__ void __launch_bounds__(Walk<S>::NT, Walk<S>::kCtas) scan_bwd_kernel(c
   if (live) {
 #pragma unroll
     for (int q = 0; q < 2; ++q) {
-      store_pairs<2>(a.da_part + un.slot * ds + so + q * S, dA[q]);
-      if (un.first && a.d_init) store_pairs<2>(a.d_init + un.n * ds + so + q * S, carry[q]);
+      store_pairs(a.da_part + un.slot * ds + so + q * S, dA[q]);
+      if (un.first && a.d_init) store_pairs(a.d_init + un.n * ds + so + q * S, carry[q]);
     }
   }
   // dD and ddelta_bias: over the threads of a channel group, in token order
@@ -707,7 +708,8 @@ kda_status kda_selective_scan_bwd(const void* x, int64_t x_stride, const void* d
   a.seg = p.m;
   const int64_t tok_blocks = (n * G * (2 * S / 4) + 255) / 256;
   const int64_t sum_blocks = ((int64_t)D * S + 2 * D + 255) / 256;
-  if ((int64_t)a.seg.units * channel_blocks(D, G, 8) > 0x7fffffffLL || tok_blocks + sum_blocks > 0x7fffffffLL ||
+  if ((int64_t)a.seg.units * channel_blocks(D, G, 8) > 0x7fffffffLL ||
+      tok_blocks + sum_blocks > 0x7fffffffLL ||
       N * D / 256 * (S / 4) > 0x7ffffff0LL)
     return KDA_ERR_UNSUPPORTED;
   char* ws = static_cast<char*>(workspace);

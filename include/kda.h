@@ -391,8 +391,9 @@ KDA_API kda_status kda_recurrent_bwd(const void *q, const void *k, const void *v
  *    a gradient runs in a fixed order, so results are deterministic.
  *  - No output may overlap an input or another output, unless the entry says
  *    so (KDA_ERR_INVALID_ARG).
- *  - cu_seqlens, num_seqs: as kda_chunk_fwd.  Malformed offsets are reported
- *    on the device (KDA_ERR_BAD_SEQLENS) and no output is written.
+ *  - B, T >= 1.  cu_seqlens, num_seqs: as kda_chunk_fwd; a workspace size is
+ *    asked for with num_seqs = 0 for a dense batch.  Malformed offsets are
+ *    reported on the device (KDA_ERR_BAD_SEQLENS) and no output is written.
  * ------------------------------------------------------------------------ */
 
 typedef enum kda_activation { KDA_ACT_NONE = 0, KDA_ACT_SILU = 1 } kda_activation;
@@ -462,7 +463,8 @@ KDA_API kda_status kda_short_conv_bwd(const void *x, int64_t x_stride, const flo
  *   out       = y, or y z Sigmoid(z) with z given,      g = d / (D / G).
  *  x, delta, z : in_dtype [B, T, D] rows (z may be NULL)
  *  Bm, Cm      : in_dtype [B, T, G, S] rows of G * S
- *  A           : fp32 [D, S] (negative where the state decays)
+ *  A           : fp32 [D, S] (negative where the state decays; a state whose
+ *                growth over some tokens passes the fp32 range is inf or NaN)
  *  D_skip, delta_bias : fp32 [D] or NULL (zeros)
  *  init_state, final_state : fp32 [N, D, S] or NULL (N = num_seqs or B); they
  *                may be the same buffer, as in kda_chunk_fwd
