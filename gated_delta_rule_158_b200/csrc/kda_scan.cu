@@ -26,7 +26,7 @@
 // unit, 460 us for the outputs at 68 % of it and 59 % of the issue slots; both
 // kernels take as long as their exponentials and their shared-memory words one
 // after the other, and more warps a scheduler gained nothing);
-// 12,001 packed tokens x 4096 in 400 to 420 us.  One token of 256 sequences x 4096: 32
+// 12,001 packed tokens x 4096 in 400 to 450 us.  One token of 256 sequences x 4096: 32
 // us = 4.4 TB/s.  Tried and not kept: one state a thread (878 us for the long
 // prompt's outputs: its loads), a quarter of the exponentials as polynomials on
 // the multiply-add units (472 us instead of 460), tiles of 16 tokens (481 us), five
