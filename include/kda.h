@@ -391,6 +391,8 @@ KDA_API kda_status kda_recurrent_bwd(const void *q, const void *k, const void *v
  *    a gradient runs in a fixed order, so results are deterministic.
  *  - No output may overlap an input or another output, unless the entry says
  *    so (KDA_ERR_INVALID_ARG).
+ *  - A workspace belongs to one call at a time: calls, or replays of captured
+ *    graphs, that may run side by side need one each.
  *  - B, T >= 1.  cu_seqlens, num_seqs: as kda_chunk_fwd; a workspace size is
  *    asked for with num_seqs = 0 for a dense batch.  Malformed offsets are
  *    reported on the device (KDA_ERR_BAD_SEQLENS) and no output is written.
