@@ -36,7 +36,12 @@ KDA_NORM_L2 = 1
 KDA_ROT_HALVES = 0
 KDA_ROT_PAIRS = 1
 
-_current_raw_stream = torch._C._cuda_getCurrentRawStream
+
+def _current_raw_stream(dev):
+    # asked for at the call: a CPU-only torch has no such function, and the
+    # package's host side works there
+    return torch._C._cuda_getCurrentRawStream(dev)
+
 
 _VP = ctypes.c_void_p
 _I = ctypes.c_int
