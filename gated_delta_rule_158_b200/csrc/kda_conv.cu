@@ -753,9 +753,8 @@ kda_status kda_short_conv_step(const void* x, int64_t x_stride, const float* wei
 }
 
 size_t kda_short_conv_bwd_workspace_size(int B, int T, int D, int W, int num_seqs) {
-  (void)num_seqs;
   if (B <= 0 || T <= 0 || D <= 0 || D % 8 != 0 || D > (1 << 24) || W < 2 || W > 4 ||
-      (int64_t)B * T > kMaxRows)
+      (int64_t)B * T > kMaxRows || num_seqs < 0 || num_seqs > kMaxRows)
     return 0;
   const int64_t total = (int64_t)B * T;
   const int64_t strips = (total + bwd_strip(total, D) - 1) / bwd_strip(total, D);

@@ -48,7 +48,8 @@ inline bool stride_ok(int64_t stride, int64_t width, int64_t esz) {
   return stride >= width && stride <= ((int64_t)1 << 31) && stride * esz % 16 == 0;
 }
 
-// B * T is a 32-bit row count, with room above it for a kernel's look-ahead
+// B * T and the number of packed sequences are 32-bit counts, with room above
+// them for a kernel's look-ahead
 constexpr int64_t kMaxRows = 0x7fff0000LL;
 
 // B, T and the packed batch's arguments
@@ -59,7 +60,7 @@ inline kda_status check_batch(const int32_t* cu, int num_seqs, int B, int T) {
   } else if (num_seqs != 0 && num_seqs != B) {
     return KDA_ERR_INVALID_ARG;
   }
-  if ((int64_t)B * T > kMaxRows) return KDA_ERR_UNSUPPORTED;
+  if ((int64_t)B * T > kMaxRows || num_seqs > kMaxRows) return KDA_ERR_UNSUPPORTED;
   return KDA_OK;
 }
 

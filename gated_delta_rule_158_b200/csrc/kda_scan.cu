@@ -720,7 +720,7 @@ Segments plan_segments(const int32_t* cu, int num_seqs, int B, int T, int D, int
   if (cu) {
     m.wide = true;
     len = T * per_seq / (kSms * 32);
-    if (len < 64) len = 64;
+    if (len < kMinSeg) len = kMinSeg;
     len = (len + kTile - 1) / kTile * kTile;
     const int64_t above = 6 * len < 512 ? 512 : 6 * len;  // shorter: the extra launches
     m.cut_above = (int)(above < T ? above : T);
@@ -729,7 +729,7 @@ Segments plan_segments(const int32_t* cu, int num_seqs, int B, int T, int D, int
     m.wide = warps >= kSms * 6;
     if (warps < kSms * (bwd ? 32 : 3)) {
       int64_t segs = kSms * (bwd ? 32 : 16) / warps;
-      if (segs > T / 64) segs = T / 64;
+      if (segs > T / kMinSeg) segs = T / kMinSeg;
       if (segs >= 2) {
         m.wide = true;
         len = (T + segs - 1) / segs;
@@ -791,7 +791,7 @@ extern "C" {
 
 size_t kda_selective_scan_fwd_workspace_size(int B, int T, int D, int S, int G, int num_seqs) {
   if (B <= 0 || T <= 0 || D <= 0 || G <= 0 || num_seqs < 0 || !sizes_ok(D, S, G) ||
-      (int64_t)B * T > kMaxRows)
+      (int64_t)B * T > kMaxRows || !units_ok(num_seqs, T))
     return 0;
   static const int32_t packed = 0;  // only whether there are offsets matters here
   const Segments m = plan_segments(num_seqs > 0 && B == 1 ? &packed : nullptr, num_seqs, B, T,
@@ -815,6 +815,7 @@ kda_status kda_selective_scan_fwd(const void* x, int64_t x_stride, const void* d
                                   size_t workspace_bytes, void* stream) {
   if (!x || !delta || !A || !Bm || !Cm || !out || !workspace) return KDA_ERR_INVALID_ARG;
   if (kda_status s = check_batch(cu_seqlens, num_seqs, B, T)) return s;
+  if (!units_ok(num_seqs, T)) return KDA_ERR_UNSUPPORTED;
   if (kda_status s = check_scan(in_dtype, D, S, G, x_stride, delta_stride, B_stride, C_stride, z,
                                 z_stride))
     return s;

@@ -274,6 +274,9 @@ __device__ __forceinline__ void load_sums(const float* row, int c, int t, float 
 // Tokens per segment, the units of a batch (kda_scan.cu).
 Segments plan_segments(const int32_t* cu, int num_seqs, int B, int T, int D, int S, bool bwd);
 bool sizes_ok(int D, int S, int G);
+// a packed batch has up to num_seqs + T / kMinSeg units, a 32-bit count
+constexpr int kMinSeg = 64;
+inline bool units_ok(int num_seqs, int T) { return (int64_t)num_seqs + T / kMinSeg <= kMaxRows; }
 inline size_t align256(size_t b) { return (b + 255) / 256 * 256; }
 
 // Packed batches: validates the offsets, chooses seg_len and writes seg_off and

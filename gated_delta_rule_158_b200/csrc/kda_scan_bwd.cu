@@ -656,7 +656,7 @@ extern "C" {
 
 size_t kda_selective_scan_bwd_workspace_size(int B, int T, int D, int S, int G, int num_seqs) {
   if (B <= 0 || T <= 0 || D <= 0 || G <= 0 || num_seqs < 0 || !sizes_ok(D, S, G) ||
-      (int64_t)B * T > kMaxRows)
+      (int64_t)B * T > kMaxRows || !units_ok(num_seqs, T))
     return 0;
   static const int32_t packed = 0;  // only whether there are offsets matters here
   return plan_bwd(num_seqs > 0 && B == 1 ? &packed : nullptr, num_seqs, B, T, D, S, G).total;
@@ -678,6 +678,7 @@ kda_status kda_selective_scan_bwd(const void* x, int64_t x_stride, const void* d
     return KDA_ERR_INVALID_ARG;
   if ((z != nullptr) != (dz != nullptr)) return KDA_ERR_INVALID_ARG;
   if (kda_status s = check_batch(cu_seqlens, num_seqs, B, T)) return s;
+  if (!units_ok(num_seqs, T)) return KDA_ERR_UNSUPPORTED;
   if (kda_status s = check_scan(in_dtype, D, S, G, x_stride, delta_stride, B_stride, C_stride, z,
                                 z_stride))
     return s;

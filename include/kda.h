@@ -393,8 +393,9 @@ KDA_API kda_status kda_recurrent_bwd(const void *q, const void *k, const void *v
  *    so (KDA_ERR_INVALID_ARG).
  *  - A workspace belongs to one call at a time: calls, or replays of captured
  *    graphs, that may run side by side need one each.
- *  - B, T >= 1.  cu_seqlens, num_seqs: as kda_chunk_fwd; a workspace size is
- *    asked for with num_seqs = 0 for a dense batch.  Malformed offsets are
+ *  - B, T >= 1.  cu_seqlens, num_seqs: as kda_chunk_fwd, at most 2^31 - 2^16
+ *    sequences (the scan: T / 64 fewer); a workspace size is asked for with
+ *    num_seqs = 0 for a dense batch.  Malformed offsets are
  *    reported on the device (KDA_ERR_BAD_SEQLENS) and no output is written.
  * ------------------------------------------------------------------------ */
 
