@@ -31,8 +31,6 @@
 // prompt's outputs: its loads), a quarter of the exponentials as polynomials on
 // the multiply-add units (472 us instead of 460), tiles of 16 tokens (481 us), five
 // or six CTAs an SM (462 us).
-#include <math.h>
-
 #include "kda_scan.cuh"
 
 namespace kda {
@@ -127,7 +125,7 @@ __global__ void __launch_bounds__(Layout<S, SC_>::NT) scan_fwd_kernel(const Args
         if (from) load_pairs(from + so + q * S, h[q]);
       }
 #pragma unroll
-      for (int i = 0; i < 4; ++i) A2[q][i] *= kLog2e;
+      for (int i = 0; i < 4; ++i) A2[q][i] = rate2(A2[q][i]);
     }
   }
 
@@ -387,8 +385,10 @@ __global__ void __launch_bounds__(256) scan_combine_kernel(const Args a) {
   const int u0 = a.seg.cu ? __ldg(a.seg.seg_off + n) : n * a.seg.segs;
   const int u1 = a.seg.cu ? __ldg(a.seg.seg_off + n + 1) : u0 + a.seg.segs;
   const int64_t ds = (int64_t)a.D * a.S;
-  float A[4], in[4] = {};
-  load_vec<float, 4>(a.A + e, A);
+  float A2[4], in[4] = {};
+  load_vec<float, 4>(a.A + e, A2);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) A2[i] = rate2(A2[i]);
   if (a.init) load_vec<float, 4>(a.init + n * ds + e, in);
   // eight segments' values in flight: the chain itself is a multiply-add each
   constexpr int U = 8;
@@ -407,7 +407,7 @@ __global__ void __launch_bounds__(256) scan_combine_kernel(const Args a) {
       if (ua + k >= u1) break;
       store_vec<4>(a.h_seg + (ua + k) * ds + e, in);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) in[i] = fmaf(ex2(w[k] * (A[i] * kLog2e)), in[i], own[k][i]);
+      for (int i = 0; i < 4; ++i) in[i] = fmaf(ex2(w[k] * A2[i]), in[i], own[k][i]);
     }
   }
   if (!a.g_seg) return;
@@ -429,7 +429,7 @@ __global__ void __launch_bounds__(256) scan_combine_kernel(const Args a) {
       if (ua - k < u0) break;
       store_vec<4>(a.g_seg + (ua - k) * ds + e, in);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) in[i] = fmaf(ex2(w[k] * (A[i] * kLog2e)), in[i], own[k][i]);
+      for (int i = 0; i < 4; ++i) in[i] = fmaf(ex2(w[k] * A2[i]), in[i], own[k][i]);
     }
   }
 }
@@ -478,7 +478,7 @@ __global__ void __launch_bounds__(256) scan_step_kernel(const Args a, float* sta
   }
   if (ns > 0) load_vec<float, 4>(a.A + so, A2);
 #pragma unroll
-  for (int i = 0; i < 4; ++i) A2[i] *= kLog2e;
+  for (int i = 0; i < 4; ++i) A2[i] = rate2(A2[i]);
   step_sizes<1>(dt, a.softplus);
   const float u = dt[0] * x;
   float y[4] = {};

@@ -2,6 +2,9 @@
 // of work, arguments, packed fp32 arithmetic.
 #pragma once
 
+#include <float.h>
+#include <math.h>
+
 #include "kda_layer.cuh"
 
 namespace kda {
@@ -130,6 +133,13 @@ inline int channel_blocks(int D, int G, int CT) { return G * ((D / G + CT - 1) /
 // rms error 3.7e-8): the exponent is raised by that much.  dt = 0 still gives
 // exactly 1.
 constexpr float kNudge = 2.9e-8f;
+// A log2 e.  Where that is -inf (a state that keeps nothing) it is the lowest
+// finite value: the tokens behind a segment's end have dt = 0, and 0 * inf would
+// be NaN; any dt above 2^-120 still gives 0.
+__device__ __forceinline__ float rate2(float A) {
+  const float r = A * kLog2e;
+  return r == -INFINITY ? -FLT_MAX : r;
+}
 __device__ __forceinline__ float decay(float dt, float A2) { return ex2(fmaf(dt, A2, kNudge)); }
 __device__ __forceinline__ f2 decay_exp(f2 dt, f2 A2) {
   return fma2(dt, A2, pack2(kNudge, kNudge));

@@ -30,8 +30,6 @@
 // tile took 1715 us; the walk in one wave of CTAs instead of four, 750 us; three
 // warps a scheduler at 168 registers spill (800 us); dt, u and dy stored twice,
 // so that the pairs need no moves, load half as much again (771 us).
-#include <math.h>
-
 #include "kda_scan.cuh"
 
 namespace kda {
@@ -194,8 +192,12 @@ __global__ void __launch_bounds__(Walk<S>::NT, Walk<S>::kCtas) scan_bwd_kernel(c
         load_pairs(a.h_seg + un.slot * ds + so + q * S, hin);
         store_pairs(own_hin + q * 4 * NT, hin);
       }
-      A2[q][0] = mul2(A2[q][0], pack2(kLog2e, kLog2e));
-      A2[q][1] = mul2(A2[q][1], pack2(kLog2e, kLog2e));
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        float lo, hi;
+        unpack2(A2[q][k], lo, hi);
+        A2[q][k] = pack2(rate2(lo), rate2(hi));
+      }
     }
   }
 

@@ -466,8 +466,9 @@ KDA_API kda_status kda_short_conv_bwd(const void *x, int64_t x_stride, const flo
  *   out       = y, or y z Sigmoid(z) with z given,      g = d / (D / G).
  *  x, delta, z : in_dtype [B, T, D] rows (z may be NULL)
  *  Bm, Cm      : in_dtype [B, T, G, S] rows of G * S
- *  A           : fp32 [D, S] (negative where the state decays; a state whose
- *                growth over some tokens passes the fp32 range is inf or NaN)
+ *  A           : fp32 [D, S] (negative where the state decays; -inf: the state
+ *                keeps nothing over a token with dt > 0; a state whose growth
+ *                over some tokens passes the fp32 range is inf or NaN)
  *  D_skip, delta_bias : fp32 [D] or NULL (zeros)
  *  init_state, final_state : fp32 [N, D, S] or NULL (N = num_seqs or B); they
  *                may be the same buffer, as in kda_chunk_fwd
