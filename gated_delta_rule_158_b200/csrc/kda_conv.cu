@@ -151,16 +151,14 @@ __device__ __forceinline__ void push_row(f2 (*win)[P], const f2 (&row)[P]) {
 template <int W, int V>
 __device__ __forceinline__ void load_taps(const ConvArgs& a, int c, f2 (&w)[W][V / 2],
                                           f2 (&b)[V / 2]) {
-  // V * W consecutive floats; c is a multiple of V, so V * W floats are a whole
-  // number of 8- or 16-byte pieces
+  // V * W consecutive floats; c is a multiple of V, and V of 4: whole 16-byte pieces
   float flat[V * W], bias[V] = {};
-  constexpr int P = V * W % 4 == 0 ? 4 : 2;
 #pragma unroll
-  for (int i = 0; i < V * W; i += P) {
-    float f[P];
-    load_vec<float, P>(a.weight + (int64_t)c * W + i, f);
+  for (int i = 0; i < V * W; i += 4) {
+    float f[4];
+    load_vec<float, 4>(a.weight + (int64_t)c * W + i, f);
 #pragma unroll
-    for (int j = 0; j < P; ++j) flat[i + j] = f[j];
+    for (int j = 0; j < 4; ++j) flat[i + j] = f[j];
   }
   if (a.bias) load_vec<float, V>(a.bias + c, bias);
 #pragma unroll

@@ -233,24 +233,19 @@ __device__ __forceinline__ f2 sigmoid2(f2 x) {
 }
 
 // ------------------------------------------------------- asynchronous copies
-// BYTES (4, 8, 16 or 32) from global to shared memory without registers; zeros
+// BYTES (4, 8 or 16) from global to shared memory without registers; zeros
 // where !in (the source is not read then)
 template <int BYTES>
 __device__ __forceinline__ void copy_in(char* to, const void* from, bool in) {
-  constexpr int N = BYTES < 16 ? BYTES : 16;
-#pragma unroll
-  for (int i = 0; i < BYTES; i += N) {
-    const uint32_t dst = (uint32_t)__cvta_generic_to_shared(to + i);
-    const char* src = static_cast<const char*>(from) + i;
-    if constexpr (N == 16)
-      asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
-                   "r"(in ? 16 : 0)
-                   : "memory");
-    else
-      asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(dst), "l"(src), "n"(N),
-                   "r"(in ? N : 0)
-                   : "memory");
-  }
+  const uint32_t dst = (uint32_t)__cvta_generic_to_shared(to);
+  if constexpr (BYTES == 16)
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(from),
+                 "r"(in ? 16 : 0)
+                 : "memory");
+  else
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(dst), "l"(from),
+                 "n"(BYTES), "r"(in ? BYTES : 0)
+                 : "memory");
 }
 __device__ __forceinline__ void copies_issued() {
   asm volatile("cp.async.commit_group;" ::: "memory");
@@ -304,10 +299,6 @@ struct Raw {
       for (int i = 0; i < N; i += 4)
         reinterpret_cast<uint4*>(p)[i / 4] = make_uint4(r[i], r[i + 1], r[i + 2], r[i + 3]);
     }
-  }
-  __device__ __forceinline__ void get(float (&v)[V]) const {
-#pragma unroll
-    for (int i = 0; i < V; ++i) v[i] = at(i);
   }
   __device__ __forceinline__ float at(int i) const {
     if constexpr (sizeof(T) == 4) return __uint_as_float(r[i]);

@@ -96,9 +96,9 @@ __global__ void __launch_bounds__(Layout<S, SC_>::NT) scan_fwd_kernel(const Args
   const Unit un = resolve(a.seg, a.sb, ub);
   // of a packed batch's gradients kEnds runs the cut ones and kEnd the others
   if (MODE != kOut && a.g_seg && a.seg.cu && un.valid && un.cut != (MODE == kEnds)) return;
-  // a sequence's last segment has no successor that needs its end state, its
-  // first none in front that needs its gradient; the checkpoints all do
-  if (!un.valid || (MODE != kOut && !a.ckpt && un.last && (MODE == kEnd || un.first))) return;
+  // a sequence's last segment has no successor that needs its end state; the
+  // gradients (with a.ckpt) need what it keeps on the way
+  if (!un.valid || (MODE == kEnd && !a.ckpt && un.last)) return;
   const int tid = threadIdx.x, nl = tid % LN, cp = tid / LN;
   const Channels ch = channels_of<CT>(a, blockIdx.x - ub * nblk);
   const int d = ch.d0 + SC * cp;

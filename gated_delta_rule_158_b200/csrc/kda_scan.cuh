@@ -252,13 +252,9 @@ __device__ __forceinline__ void store_sums(float* entry, const float (&v)[SC][4]
 #pragma unroll
   for (int q = 0; q < SC; ++q) r[q] = sum_lanes<LN>(v[q], l);
   if constexpr (SC == 2) {
-    if constexpr (LN == 2) {
-      float* at = entry + 2 * l * P + 2 * l;
-      *reinterpret_cast<float2*>(at) = make_float2(r[0].x, r[1].x);
-      *reinterpret_cast<float2*>(at + P) = make_float2(r[0].y, r[1].y);
-    } else if (l < 4) {
+    static_assert(LN >= 4, "8 states have one channel a thread");
+    if (l < 4)
       *reinterpret_cast<float2*>(entry + l * P + (l & 2)) = make_float2(r[0].x, r[1].x);
-    }
   } else {
     if constexpr (LN == 2) {
       entry[2 * l * P] = r[0].x;
