@@ -31,7 +31,7 @@ constexpr int kNormThreads = 256;
 template <typename Tin>
 constexpr int kRows = 8 / (int)sizeof(Tin);
 constexpr int kBwdRows = 2;
-constexpr int kMaxTokens = 16;  // tokens per tile (two shared tables: 2 x 16 x 256 floats)
+constexpr int kMaxTokens = 16;  // rotated tokens per tile (two shared tables: 2 x 16 x 256 floats)
 
 struct NormArgs {
   const void* q;
@@ -427,35 +427,34 @@ __global__ void __launch_bounds__(256) qk_norm_bwd_sum_kernel(const float* __res
 
 int lane_group(int d) { return d <= 32 ? 4 : d <= 64 ? 8 : d <= 128 ? 16 : 32; }
 
-// The split of a block's lane groups into heads and tokens, and the tokens per
-// tile.  HS is the number that leaves the fewest group steps empty over the
-// heads; a tile is U TS tokens, fewer where that would leave SMs without one.
-void tile_shape(NormArgs& a, int rows) {
+constexpr int kFwdBlocks = 148 * 4, kBwdBlocks = 148 * 2;  // as many as are resident
+
+// The split of a block's lane groups into HS heads x TS tokens, and the tokens
+// per tile: up to U TS, no more than give every resident block one, nor (with a
+// rotation) than the tables hold.  The split with the most rows in flight in a
+// block is taken, the one with the most heads of several.  Measured, bf16, forward
+// and gradients: 16,384 tokens x 2 heads x 32, 8 and 12 us (with one token a step
+// as soon as TS is above a block's share, 22 and 55); 9000 x 9 x 128, 16 and 33 us
+// (16 and 43; with the split that leaves the fewest lanes idle, 23 and 33).
+void tile_shape(NormArgs& a, int rows, int blocks) {
   const int H = a.Hq + a.Hk, groups = kNormThreads / lane_group(a.d);
-  int best = 1;
-  int64_t most = 0;
+  int most = (int)(((int64_t)a.tokens + blocks - 1) / blocks);
+  if (a.rot && most > kMaxTokens) most = kMaxTokens;
+  int64_t best = 0;
   for (int hs = 1; hs <= groups && hs <= H; ++hs) {
-    // heads per step and group, times 2^20
-    const int64_t used = ((int64_t)H << 20) / ((H + hs - 1) / hs) * (groups / hs) / groups;
-    if (used >= most) {
-      most = used;
-      best = hs;
+    const int ts = groups / hs < most ? groups / hs : most;
+    const int n = rows * ts < most ? rows * ts : most;
+    // heads per step, times 2^20, by tokens
+    const int64_t rows_in_flight = ((int64_t)H << 20) / ((H + hs - 1) / hs) * n;
+    if (rows_in_flight >= best) {
+      best = rows_in_flight;
+      a.hs = hs;
+      a.ts = ts;
+      a.per_block = n;
     }
   }
-  a.hs = best;
-  a.ts = groups / best;
-  const int even = a.tokens / (148 * 4);  // a tile for every resident block
-  if (even < a.ts) {
-    a.hs = groups < H ? groups : H;
-    a.ts = 1;
-  }
-  int n = rows * a.ts;
-  if (n > even) n = even;
-  if (n > kMaxTokens) n = kMaxTokens;
-  a.per_block = n < 1 ? 1 : n;
 }
 
-constexpr int kFwdBlocks = 148 * 4, kBwdBlocks = 148 * 2;  // as many as are resident
 size_t table_bytes(const NormArgs& a) { return 2 * sizeof(float) * (size_t)a.per_block * a.rot; }
 
 template <typename Tin, int ROT>
@@ -580,7 +579,7 @@ kda_status kda_qk_norm_fwd(const void* q, int64_t q_stride, const void* k, int64
                          tokens, Hq, Hk, d, rot_dim, norm, rotation, eps);
   a.q_out = q_out;
   a.k_out = k_out;
-  tile_shape(a, in_dtype == KDA_BF16 ? kRows<__nv_bfloat16> : kRows<float>);
+  tile_shape(a, in_dtype == KDA_BF16 ? kRows<__nv_bfloat16> : kRows<float>, kFwdBlocks);
   cudaStream_t st = (cudaStream_t)stream;
   const cudaError_t e = in_dtype == KDA_BF16 ? dispatch_fwd<__nv_bfloat16>(a, st)
                                              : dispatch_fwd<float>(a, st);
@@ -637,7 +636,7 @@ kda_status kda_qk_norm_bwd(const void* q, int64_t q_stride, const void* k, int64
   a.dq = dq;
   a.dk = dk;
   a.partial = sums ? static_cast<float*>(workspace) : nullptr;
-  tile_shape(a, kBwdRows);
+  tile_shape(a, kBwdRows, kBwdBlocks);
   const int64_t tiles = ((int64_t)tokens + a.per_block - 1) / a.per_block;
   a.blocks = (int)(tiles < kBwdBlocks ? tiles : kBwdBlocks);
   cudaStream_t st = (cudaStream_t)stream;

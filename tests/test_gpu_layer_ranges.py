@@ -7,7 +7,7 @@ import gated_delta_rule_158_b200 as kda
 
 import layer_ref as R
 from test_gpu_layer_edges import scan_backward, scan_forward
-from test_gpu_layer_ops import (DEV, F32, flat, host, near, ok, scan_inputs, scan_opt,
+from test_gpu_layer_ops import (BF16, DEV, F32, draw, flat, host, near, ok, scan_inputs, scan_opt,
                                 scan_ref)
 
 pytestmark = pytest.mark.gpu
@@ -60,3 +60,70 @@ def test_scan_states_that_keep_nothing(B, T, D, S, cu):
         _, ro, rf = scan_ref(dict(ref, bounds=R.seq_bounds(B, 1, None), **cut))
         near(out, ro)
         near(state, rf)
+
+
+# ------------------------------------------------------------------- norms
+def norm_call(T, Hq, Hk, d, rot, dtype, seed=6):
+    gen = torch.Generator().manual_seed(seed)
+    t = dict(q=draw(gen, T, Hq, d, dtype=dtype), k=draw(gen, T, Hk, d, dtype=dtype),
+             dq=draw(gen, T, Hq, d), dk=draw(gen, T, Hk, d))
+    opt = dict(q_weight=0.5 + torch.rand(d, generator=gen).to(DEV),
+               k_weight=0.5 + torch.rand(d, generator=gen).to(DEV), mode=kda.KDA_NORM_RMS)
+    if rot:
+        opt.update(positions=torch.arange(T, dtype=torch.int32, device=DEV),
+                   inv_freq=torch.rand(rot // 2, generator=gen).to(DEV))
+    e = lambda x, dt=F32: torch.full(x.shape, float("nan"), dtype=dt, device=DEV)  # noqa: E731
+    out = dict(q=e(t["q"], dtype), k=e(t["k"], dtype))
+    g = dict(dq=e(t["q"]), dk=e(t["k"]), dq_weight=e(opt["q_weight"]), dk_weight=e(opt["k_weight"]))
+    ws = torch.empty(kda.kda_qk_norm_bwd_workspace_size(T, Hq, Hk, d), dtype=torch.uint8,
+                     device=DEV)
+    fwd = lambda: kda.kda_qk_norm_fwd(t["q"], t["k"], out["q"], out["k"], **opt)  # noqa: E731
+    bwd = lambda: kda.kda_qk_norm_bwd(t["q"], t["k"], t["dq"], t["dk"], g, ws, **opt)  # noqa: E731
+    return t, opt, out, g, fwd, bwd
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("T,Hq,Hk,d,rot", [
+    # few heads: tiles of many tokens, of all sizes around a tile for every block
+    (9473, 1, 1, 32, 0), (9473, 1, 1, 32, 32), (2401, 1, 2, 64, 0), (1777, 1, 1, 8, 0),
+    (593, 3, 1, 96, 96), (297, 1, 1, 32, 16),
+    # more heads than fit beside one another, and as many
+    (1201, 8, 1, 128, 0), (1185, 9, 8, 128, 128), (700, 5, 3, 256, 64), (1185, 40, 24, 16, 16),
+])
+def test_norm_tiles(T, Hq, Hk, d, rot, dtype):
+    t, opt, out, g, fwd, bwd = norm_call(T, Hq, Hk, d, rot, dtype)
+    fwd()
+    bwd()
+    freq = opt["inv_freq"].cpu() if rot else None
+    for n in ("q", "k"):
+        x, w = host(t[n], True), host(opt[n + "_weight"], True)
+        y = R.norm(x, w, torch.arange(T), freq, False, False, 1e-6)
+        near(out[n], y, dtype, n)
+        y.backward(host(t["d" + n]))
+        near(g["d" + n], x.grad, what="d" + n)
+        near(g[f"d{n}_weight"], w.grad, what=n + " weight")
+
+
+def microseconds(f):
+    for _ in range(3):
+        f()
+    times = []
+    for _ in range(30):
+        a, b = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+        torch.cuda.synchronize()
+        a.record()
+        f()
+        b.record()
+        torch.cuda.synchronize()
+        times.append(a.elapsed_time(b) * 1e3)
+    return min(times)
+
+
+@pytest.mark.parametrize("rot", [0, 32])
+def test_norm_of_fewer_tokens_takes_no_longer(rot):
+    """16,384 tokens of two short heads against 40,000: less than half the work.
+    (With one token a step and block, most lanes idle, they took three times as long.)"""
+    few = norm_call(16384, 1, 1, 32, rot, BF16)[-2:]
+    many = norm_call(40000, 1, 1, 32, rot, BF16)[-2:]
+    for a, b in zip(few, many):
+        assert microseconds(a) <= 1.5 * microseconds(b)
