@@ -511,9 +511,10 @@ __global__ void __launch_bounds__(256) scan_step_kernel(const Args a, float* sta
 }
 
 // Packed batches: validates the offsets, then chooses the segment length
-// (seg_len where a sequence is longer than cut_above, else the whole batch's
-// length, so that every sequence is one unit) and writes seg_off and order.
+// (seg_len or more where a sequence is longer than cut_above, else the whole
+// batch's length, so that every sequence is one unit) and writes seg_off and order.
 constexpr int kMaxOrder = 2048;
+constexpr int kMaxSegs = 148;  // of a sequence (plan_segments)
 
 __global__ void __launch_bounds__(1024) scan_plan_kernel(const int32_t* __restrict__ cu, int N,
                                                          int T, StatusBlock* sb, int cut_above,
@@ -543,10 +544,14 @@ __global__ void __launch_bounds__(1024) scan_plan_kernel(const int32_t* __restri
     sb->detail = 0;
     sb->never_set = 0;
     sb->seqlens_ok = bad ? 0 : 1;
-    sb->pad[0] = longest > cut_above ? seg_len : T;
   }
   if (bad) return;
-  const int sl = longest > cut_above ? seg_len : T;
+  int sl = T;
+  if (longest > cut_above) {  // no more than kMaxSegs of any sequence
+    sl = (longest - 1) / (kMaxSegs * kTile) * kTile + kTile;
+    if (sl < seg_len) sl = seg_len;
+  }
+  if (tid == 0) sb->pad[0] = sl;
   // longest first; batches of more sequences keep their order
   for (int n = tid; n < N; n += 1024) {
     int rank = n;
@@ -700,7 +705,11 @@ bool sizes_ok(int D, int S, int G) {
 //     199, 159 at 2.6).
 // The gradients' first pass over the segments is needed anyway and their walk
 // has two warps a scheduler at most: cut until there are SMs x 32 warps, four
-// waves (493 us; 555 with SMs x 8 or 16 at 3.5 warps an SM).
+// waves (493 us; 555 with SMs x 8 or 16 at 3.5 warps an SM).  A sequence has
+// kMaxSegs segments at most: their combination is one chain, 0.1 us a segment and
+// 0.4 in the gradients (65,536 tokens x 64 channels, forward and gradients: 107
+// and 226 us, 138 and 552 with 512 and 1024 segments; gradients of 16,384 x 256
+// in 202 us, 253 with 256 segments).
 // Packed batches do not show their lengths to the host: two channels a thread,
 // and a cut (the plan kernel's choice) into halves of the even share of SMs x
 // 16 warps, where one sequence is longer than three shares.  12,000 tokens x
@@ -730,6 +739,7 @@ Segments plan_segments(const int32_t* cu, int num_seqs, int B, int T, int D, int
     if (warps < kSms * (bwd ? 32 : 3)) {
       int64_t segs = kSms * (bwd ? 32 : 16) / warps;
       if (segs > T / kMinSeg) segs = T / kMinSeg;
+      if (segs > kMaxSegs) segs = kMaxSegs;
       if (segs >= 2) {
         m.wide = true;
         len = (T + segs - 1) / segs;

@@ -127,3 +127,31 @@ def test_norm_of_fewer_tokens_takes_no_longer(rot):
     many = norm_call(40000, 1, 1, 32, rot, BF16)[-2:]
     for a, b in zip(few, many):
         assert microseconds(a) <= 1.5 * microseconds(b)
+
+
+# ------------------------------------------------- one long sequence, few channels
+@pytest.mark.parametrize("cu", [None, [0, 11000, 12000]])
+def test_scan_of_a_long_sequence(cu):
+    """More tokens than a sequence's segments times the shortest segment: the
+    segments are longer, in dense and in packed batches."""
+    B, T, D, S = 1, 12000, 8, 8
+    i = scan_inputs((B, T, D, S, 1, cu, True, True, True, True, True, False), F32, seed=17)
+    check_scan(i, B, T, D, S, 1, F32)
+
+
+@pytest.mark.parametrize("packed", [False, True])
+def test_scan_gradients_of_four_times_the_tokens(packed):
+    """65,536 tokens of 64 channels against 16,384.  (Cut into 1024 segments, whose
+    combination is one chain, they took 3.8 times as long.)"""
+    def backward(T, D=64, S=16):
+        gen = torch.Generator(device=DEV).manual_seed(1)
+        n = lambda *s: torch.randn(s, generator=gen, device=DEV).to(BF16)  # noqa: E731
+        x, bc = n(1, T, D), n(1, T, 1, S)
+        A = -0.1 - torch.rand(D, S, generator=gen, device=DEV)
+        e = lambda *s: torch.empty(s, device=DEV)  # noqa: E731
+        g = dict(dx=e(1, T, D), ddelta=e(1, T, D), dA=e(D, S), dB=e(1, T, 1, S), dC=e(1, T, 1, S))
+        cu = torch.tensor([0, T], dtype=torch.int32, device=DEV) if packed else None
+        ws = torch.empty(kda.kda_selective_scan_bwd_workspace_size(1, T, D, S, 1, int(packed)),
+                         dtype=torch.uint8, device=DEV)
+        return lambda: kda.kda_selective_scan_bwd(x, x, A, bc, bc, x, g, ws, cu_seqlens=cu)
+    assert microseconds(backward(65536)) <= 3 * microseconds(backward(16384))
