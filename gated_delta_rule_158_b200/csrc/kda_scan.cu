@@ -512,8 +512,12 @@ __global__ void __launch_bounds__(256) scan_step_kernel(const Args a, float* sta
 
 // Packed batches: validates the offsets, then chooses the segment length
 // (seg_len or more where a sequence is longer than cut_above, else the whole
-// batch's length, so that every sequence is one unit) and writes seg_off and order.
-constexpr int kMaxOrder = 2048;
+// batch's length, so that every sequence is one unit) and writes seg_off and, for
+// a batch left whole, order.  Longest first pays up to kMaxOrder sequences; the
+// ranks take N^2 comparisons of one CTA.  Ordered and not, us, 16,384 tokens x
+// 1024 x 16: 159 and 211 with 64 sequences, 140 and 171 with 128, 159 and 175
+// with 256, 206 and 210 with 512, 319 and 293 with 1024, 616 and 480 with 2048.
+constexpr int kMaxOrder = 512;
 constexpr int kMaxSegs = 148;  // of a sequence (plan_segments)
 
 __global__ void __launch_bounds__(1024) scan_plan_kernel(const int32_t* __restrict__ cu, int N,
@@ -553,7 +557,7 @@ __global__ void __launch_bounds__(1024) scan_plan_kernel(const int32_t* __restri
   }
   if (tid == 0) sb->pad[0] = sl;
   // longest first; batches of more sequences keep their order
-  for (int n = tid; n < N; n += 1024) {
+  for (int n = tid; n < N && sl == T; n += 1024) {
     int rank = n;
     if (N <= kMaxOrder) {
       const int len = lens[n];

@@ -13,8 +13,8 @@ namespace scan {
 // The tokens are one flat axis; a unit is one segment (at most seg_len tokens)
 // of one sequence.  Dense: segs units per sequence.  Packed: the plan kernel
 // has chosen seg_len (in the status block) and written seg_off[n], the units
-// before sequence n, and order, the sequences longest first; with one unit per
-// sequence, unit u is sequence order[u].
+// before sequence n; with one unit per sequence (a batch left whole) unit u is
+// sequence order[u], the longest first.
 struct Segments {
   const int32_t* cu;       // nullptr = dense
   const int32_t* seg_off;  // packed

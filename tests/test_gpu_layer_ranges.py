@@ -155,3 +155,32 @@ def test_scan_gradients_of_four_times_the_tokens(packed):
                          dtype=torch.uint8, device=DEV)
         return lambda: kda.kda_selective_scan_bwd(x, x, A, bc, bc, x, g, ws, cu_seqlens=cu)
     assert microseconds(backward(65536)) <= 3 * microseconds(backward(16384))
+
+
+# ----------------------------------------------------- packed: many sequences
+def lengths(N, seed=5, most=6):
+    gen = torch.Generator().manual_seed(seed)
+    lens = torch.randint(0, most + 1, (N,), generator=gen)
+    return [0] + torch.cumsum(lens, 0).tolist()
+
+
+@pytest.mark.parametrize("N", [511, 512, 513])
+def test_scan_around_the_last_ordered_batch(N):
+    cu = lengths(N)
+    i = scan_inputs((1, cu[-1], 8, 8, 1, cu, True, True, True, True, True, False), F32, seed=N)
+    check_scan(i, 1, cu[-1], 8, 8, 1, F32)
+
+
+def test_scan_plan_of_many_sequences():
+    """2048 sequences of eight tokens against 2049.  (Ordered by N^2 comparisons, the
+    2048 took 3.6 times as long.)"""
+    def forward(N, T=16384, D=64, S=16):
+        gen = torch.Generator(device=DEV).manual_seed(1)
+        n = lambda *s: torch.randn(s, generator=gen, device=DEV).to(BF16)  # noqa: E731
+        x, bc = n(1, T, D), n(1, T, 1, S)
+        A, out = -torch.ones(D, S, device=DEV), torch.empty(1, T, D, dtype=BF16, device=DEV)
+        cu = (torch.arange(N + 1, device=DEV) * T // N).to(torch.int32)
+        ws = torch.empty(kda.kda_selective_scan_fwd_workspace_size(1, T, D, S, 1, N),
+                         dtype=torch.uint8, device=DEV)
+        return lambda: kda.kda_selective_scan_fwd(x, x, A, bc, bc, out, ws, cu_seqlens=cu)
+    assert microseconds(forward(2048)) <= 1.5 * microseconds(forward(2049))
