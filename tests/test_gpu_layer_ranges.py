@@ -6,7 +6,7 @@ import torch
 import gated_delta_rule_158_b200 as kda
 
 import layer_ref as R
-from test_gpu_layer_edges import scan_backward, scan_forward
+from test_gpu_layer_edges import SPREADS, scan_backward, scan_forward
 from test_gpu_layer_ops import (BF16, DEV, F32, draw, flat, host, near, ok, scan_inputs, scan_opt,
                                 scan_ref)
 
@@ -184,3 +184,172 @@ def test_scan_plan_of_many_sequences():
                          dtype=torch.uint8, device=DEV)
         return lambda: kda.kda_selective_scan_fwd(x, x, A, bc, bc, out, ws, cu_seqlens=cu)
     assert microseconds(forward(2048)) <= 1.5 * microseconds(forward(2049))
+
+
+# --------------------------------------------------------------- types, values
+@pytest.mark.parametrize("spread", SPREADS)
+def test_scan_spreads_fp32(spread):
+    B, T, D, S, G, cu = spread
+    i = scan_inputs((B, T, D, S, G, cu, True, True, True, True, True, False), F32, seed=33)
+    check_scan(i, B, T, D, S, G, F32)
+
+
+def test_softplus_of_special_values():
+    """One token, A = 0, unit B and C in one state: y = softplus(v) itself, by the
+    prompt's kernel and by the step's.  e^-|v| is off by (2 + |v|) 2^-22 (the
+    exponential and its rounded argument), the polynomial by 1.5e-7, the additions
+    by 2^-23.  Below -87.3 e^v is no normal fp32 number, and 0."""
+    v = torch.tensor([-1e-30, 0.0, 1e-30, 88.0, 1e-6, -1e-6, 0.5, -0.5, -5.0, 5.0, -16.0, 16.0,
+                      -17.5, -80.0, 1000.0, -1000.0], device=DEV)
+    D = v.numel()
+    one = torch.zeros(1, 1, 1, 8, device=DEV)
+    one[..., 0] = 1
+    A, x = torch.zeros(D, 8, device=DEV), torch.ones(1, 1, D, device=DEV)
+    out, step = torch.empty(1, 1, D, device=DEV), torch.empty(1, D, device=DEV)
+    ws = torch.empty(kda.kda_selective_scan_fwd_workspace_size(1, 1, D, 8), dtype=torch.uint8,
+                     device=DEV)
+    kda.kda_selective_scan_fwd(x, v.view(1, 1, D), A, one, one, out, ws)
+    kda.kda_selective_scan_step(x[0], v.view(1, D), A, one[0], one[0],
+                                torch.zeros(1, D, 8, device=DEV), step)
+    v64 = v.cpu().double()
+    ref = v64.clamp(min=0) + torch.log1p(torch.exp(-v64.abs()))
+    ref[-1] = 0.0
+    bar = ref * ((2 + v64.abs().clamp(max=100)) * 2.0 ** -22 + 1.5e-7 + 2.0 ** -23)
+    for y in (out, step):
+        y = y.cpu().double().view(-1)
+        assert bool(((y - ref).abs() <= bar).all()), y - ref
+
+
+# ------------------------------------------------- steps of many sequences, fp64
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("S,D,G,N", [(16, 1032, 1, 78), (16, 1024, 4, 77), (32, 512, 2, 75),
+                                     (64, 264, 1, 75), (128, 192, 3, 50)])
+def test_scan_step_of_many_sequences(S, D, G, N, dtype):
+    """Four sequences a thread (ceil(N / 4) D S / 4 threads, above 148 x 512), the
+    last group not full, with all optional inputs."""
+    assert (N + 3) // 4 * D * S // 4 >= 148 * 512 and N % 4
+    i = scan_inputs((N, 1, D, S, G, None, True, True, True, True, True, True), dtype, seed=51)
+    state, out = i["init"].clone(), torch.full((N, D), float("nan"), dtype=dtype, device=DEV)
+    one = lambda n: i[n][:, 0]  # noqa: E731
+    kda.kda_selective_scan_step(one("x"), one("delta"), i["A"], one("Bm"), one("Cm"), state, out,
+                                **dict(scan_opt(i), z=one("z")))
+    _, ro, rf = scan_ref(i)
+    near(out, ro, dtype)
+    near(state, rf)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("Wd,silu,bias", [(2, True, True), (3, False, True), (4, False, False),
+                                          (4, True, True)])
+def test_conv_step_of_many_sequences(Wd, silu, bias, dtype):
+    """Four sequences a thread (ceil(N / 4) D / 4 threads, above 148 x 256)."""
+    N, D = 146, 4104
+    assert (N + 3) // 4 * D // 4 >= 148 * 256 and N % 4
+    gen = torch.Generator().manual_seed(52)
+    x = draw(gen, N, D, dtype=dtype)
+    w, b = draw(gen, D, Wd, scale=0.5), draw(gen, D) if bias else None
+    state = draw(gen, N, Wd - 1, D, dtype=dtype)
+    rows = torch.cat([host(state), host(x)[:, None]], 1)
+    out = torch.full((N, D), float("nan"), dtype=dtype, device=DEV)
+    kda.kda_short_conv_step(x, w, state, out, bias=b,
+                            activation=kda.KDA_ACT_SILU if silu else kda.KDA_ACT_NONE)
+    p = (rows * host(w).t()).sum(1) + (host(b) if bias else 0)
+    near(out, p * torch.sigmoid(p) if silu else p, dtype)
+    assert torch.equal(host(state), rows[:, 1:])
+
+
+# ------------------------------------------- gradients at offsets beyond 32 bits
+# the last sequence of a packed batch of more than 2^31 elements; the cotangents
+# in front of it are zero, so that the sums over all tokens are its own too
+BIG_T, BIG_D, TAIL = 263000, 8192, 300
+BIG_CU = [0, BIG_T - TAIL, BIG_T]
+
+
+def big(dtype=BF16):
+    torch.cuda.empty_cache()
+    return torch.empty(1, BIG_T, BIG_D, dtype=dtype, device=DEV)
+
+
+def last(t):
+    return t[:, BIG_T - TAIL:]
+
+
+def same(whole, alone, what):
+    # the strips and segments differ: other orders of the same sums
+    assert R.rel_l2(whole, alone) <= 1e-5, (what, R.rel_l2(whole, alone))
+
+
+def test_conv_gradients_beyond_32_bit_offsets():
+    x = big().normal_()
+    dout = big(F32).zero_()
+    last(dout).normal_()
+    w = torch.randn(BIG_D, 4, device=DEV)
+    g = dict(dx=big(F32), dweight=torch.empty_like(w), dbias=torch.empty(BIG_D, device=DEV),
+             d_init=torch.empty(2, 3, BIG_D, device=DEV))
+    ws = torch.empty(kda.kda_short_conv_bwd_workspace_size(1, BIG_T, BIG_D, 4, 2),
+                     dtype=torch.uint8, device=DEV)
+    b = torch.randn(BIG_D, device=DEV)
+    kda.kda_short_conv_bwd(x, w, dout, g, ws, bias=b,
+                           cu_seqlens=torch.tensor(BIG_CU, dtype=torch.int32, device=DEV))
+    ok(ws)
+    a = dict(dx=torch.empty(1, TAIL, BIG_D, device=DEV), dweight=torch.empty_like(w),
+             dbias=torch.empty_like(b), d_init=torch.empty(1, 3, BIG_D, device=DEV))
+    kda.kda_short_conv_bwd(last(x), w, last(dout), a, ws, bias=b)
+    same(last(g["dx"]), a["dx"], "dx")
+    assert not bool(g["dx"][:, BIG_T - TAIL - 1000:BIG_T - TAIL].any())
+    for k in ("dweight", "dbias"):
+        same(g[k], a[k], k)
+    same(g["d_init"][1:], a["d_init"], "d_init")
+
+
+def test_scan_gradients_beyond_32_bit_offsets():
+    S = 8
+    x = big().normal_()
+    dout = big().zero_()
+    last(dout).normal_()
+    bc = torch.randn(1, BIG_T, 1, S, device=DEV).to(BF16)
+    A = -torch.rand(BIG_D, S, device=DEV) - 0.1
+    f32 = lambda *s: torch.empty(s, device=DEV)  # noqa: E731
+    g = dict(dx=big(F32), ddelta=big(F32), dz=big(F32), dA=f32(BIG_D, S),
+             dB=f32(1, BIG_T, 1, S), dC=f32(1, BIG_T, 1, S), dD=f32(BIG_D),
+             ddelta_bias=f32(BIG_D), d_init=f32(2, BIG_D, S))
+    ws = torch.empty(kda.kda_selective_scan_bwd_workspace_size(1, BIG_T, BIG_D, S, 1, 2),
+                     dtype=torch.uint8, device=DEV)
+    kda.kda_selective_scan_bwd(x, x, A, bc, bc, dout, g, ws, z=x,
+                               cu_seqlens=torch.tensor(BIG_CU, dtype=torch.int32, device=DEV))
+    ok(ws)
+    a = {k: f32(1, TAIL, *g[k].shape[2:]) for k in ("dx", "ddelta", "dz", "dB", "dC")}
+    a.update({k: torch.empty_like(g[k]) for k in ("dA", "dD", "ddelta_bias")},
+             d_init=f32(1, BIG_D, S))
+    part, mix = last(x), last(bc)
+    kda.kda_selective_scan_bwd(part, part, A, mix, mix, last(dout), a, ws, z=part)
+    for k in ("dx", "ddelta", "dz", "dB", "dC"):
+        same(last(g[k]), a[k], k)
+    for k in ("dA", "dD", "ddelta_bias"):
+        same(g[k], a[k], k)
+    same(g["d_init"][1:], a["d_init"], "d_init")
+
+
+def test_norm_gradients_beyond_32_bit_offsets():
+    tokens, H, Hk, d, tail = 263000, 32, 2, 256, 300
+    torch.cuda.empty_cache()
+    q = torch.empty(tokens, H, d, dtype=BF16, device=DEV).normal_()
+    k = q[:, :Hk].contiguous()
+    dq, dk = torch.zeros(tokens, H, d, device=DEV), torch.zeros(tokens, Hk, d, device=DEV)
+    dq[-tail:].normal_()
+    dk[-tail:].normal_()
+    w = 0.5 + torch.rand(d, device=DEV)
+    pos = torch.arange(tokens, dtype=torch.int32, device=DEV)
+    opt = dict(q_weight=w, k_weight=w, inv_freq=torch.rand(32, device=DEV))
+    e = lambda *s: torch.empty(s, device=DEV)  # noqa: E731
+    a = dict(dq=e(tail, H, d), dk=e(tail, Hk, d), dq_weight=e(d), dk_weight=e(d))
+    ws = torch.empty(kda.kda_qk_norm_bwd_workspace_size(tokens, H, Hk, d), dtype=torch.uint8,
+                     device=DEV)
+    kda.kda_qk_norm_bwd(q[-tail:], k[-tail:], dq[-tail:], dk[-tail:], a, ws,
+                        positions=pos[-tail:].clone(), **opt)
+    g = dict(dq=dq, dk=dk, dq_weight=e(d), dk_weight=e(d))  # over the cotangents
+    kda.kda_qk_norm_bwd(q, k, dq, dk, g, ws, positions=pos, **opt)
+    for n in ("dq", "dk"):
+        same(g[n][-tail:], a[n], n)
+        assert not bool(g[n][-tail - 1000:-tail].any())
+        same(g[n + "_weight"], a[n + "_weight"], n + " weight")
