@@ -409,6 +409,12 @@ def _refuse(dev, name, t, shape, dtype):
         raise ValueError(f"{name}: expected a tensor on the current CUDA device")
 
 
+def _sizes(*sizes):
+    """ctypes would cut an int of more than 32 bits down without a word."""
+    if max(sizes) > 0x7FFFFFFF:
+        raise ValueError(f"sizes {sizes}: at most 2^31 - 1 each")
+
+
 def _rows(dev, name, t, shape, lead, width, dtype):
     """(pointer, row stride) of a tensor whose first `lead` dimensions number
     its rows of `width` elements: rows dense, any constant distance apart."""
@@ -456,6 +462,7 @@ def _offsets(dev, cu_seqlens, batch):
     if cu_seqlens is None:
         return None, 0, batch
     n = cu_seqlens.numel() - 1
+    _sizes(n)
     return _arg(dev, "cu_seqlens", cu_seqlens, (n + 1,), torch.int32), n, n
 
 
@@ -481,6 +488,7 @@ def kda_short_conv_fwd(x, weight, out, workspace, bias=None, init_state=None, cu
     B, T, D = shape
     W = weight.shape[-1]
     cu, num, N = _offsets(dev, cu_seqlens, B)
+    _sizes(B, T, D, W)
     xp, xs = _rows(dev, "x", x, shape, 2, D, dt)
     ws, wsb = _scratch(dev, workspace)
     _check(lib().kda_short_conv_fwd(
@@ -497,6 +505,7 @@ def kda_short_conv_step(x, weight, state, out, bias=None, activation=KDA_ACT_SIL
     shape, dt, code = x.shape, x.dtype, _dtype(x)
     N, D = shape
     W = weight.shape[-1]
+    _sizes(N, D, W)
     xp, xs = _rows(dev, "x", x, shape, 1, D, dt)
     _check(lib().kda_short_conv_step(
         xp, xs, _arg(dev, "weight", weight, (D, W), _F32T), _opt(dev, "bias", bias, (D,), _F32T),
@@ -505,6 +514,7 @@ def kda_short_conv_step(x, weight, state, out, bias=None, activation=KDA_ACT_SIL
 
 
 def kda_short_conv_bwd_workspace_size(B, T, D, W, num_seqs=0) -> int:
+    _sizes(B, T, D, W, num_seqs)
     return int(lib().kda_short_conv_bwd_workspace_size(B, T, D, W, num_seqs))
 
 
@@ -518,6 +528,7 @@ def kda_short_conv_bwd(x, weight, dout, grads, workspace, bias=None, init_state=
     B, T, D = shape
     W = weight.shape[-1]
     cu, num, N = _offsets(dev, cu_seqlens, B)
+    _sizes(B, T, D, W)
     xp, xs = _rows(dev, "x", x, shape, 2, D, dt)
     ws, wsb = _scratch(dev, workspace)
     _check(lib().kda_short_conv_bwd(
@@ -531,6 +542,7 @@ def kda_short_conv_bwd(x, weight, dout, grads, workspace, bias=None, init_state=
 
 
 def kda_selective_scan_fwd_workspace_size(B, T, D, S, G=1, num_seqs=0) -> int:
+    _sizes(B, T, D, S, G, num_seqs)
     return int(lib().kda_selective_scan_fwd_workspace_size(B, T, D, S, G, num_seqs))
 
 
@@ -539,6 +551,7 @@ def _scan_inputs(dev, x, delta, A, Bm, Cm, D, z, delta_bias, delta_softplus):
     shape, dt, code = x.shape, x.dtype, _dtype(x)
     n, ch = len(shape) - 1, shape[-1]
     (S,), (G,) = A.shape[-1:], Bm.shape[-2:-1]
+    _sizes(*shape, S, G)
     mix, w = (*shape[:-1], G, S), G * S
     return (*_rows(dev, "x", x, shape, n, ch, dt), *_rows(dev, "delta", delta, shape, n, ch, dt),
             _arg(dev, "A", A, (ch, S), _F32T), *_rows(dev, "Bm", Bm, mix, n, w, dt),
@@ -579,6 +592,7 @@ def kda_selective_scan_step(x, delta, A, Bm, Cm, state, out, D=None, z=None, del
 
 
 def kda_selective_scan_bwd_workspace_size(B, T, D, S, G=1, num_seqs=0) -> int:
+    _sizes(B, T, D, S, G, num_seqs)
     return int(lib().kda_selective_scan_bwd_workspace_size(B, T, D, S, G, num_seqs))
 
 
@@ -612,6 +626,7 @@ def _norm_inputs(dev, q, k, q_weight, k_weight, positions, inv_freq, mode, rotat
     *lead, Hq, dim = shape
     Hk = k.shape[-2]
     k_shape, n, tokens = (*lead, Hk, dim), len(lead), math.prod(lead)
+    _sizes(tokens, Hq, Hk, dim)
     rot = 0 if inv_freq is None else 2 * inv_freq.numel()
     return (*_rows(dev, "q", q, shape, n, Hq * dim, dt),
             *_rows(dev, "k", k, k_shape, n, Hk * dim, dt),
@@ -638,6 +653,7 @@ def kda_qk_norm_fwd(q, k, q_out, k_out, q_weight=None, k_weight=None, positions=
 
 
 def kda_qk_norm_bwd_workspace_size(tokens, Hq, Hk, d) -> int:
+    _sizes(tokens, Hq, Hk, d)
     return int(lib().kda_qk_norm_bwd_workspace_size(tokens, Hq, Hk, d))
 
 

@@ -1,6 +1,7 @@
 """Host side of the operators around the recurrence: limits of their sizes,
 refused before anything is launched (fake pointers, no GPU)."""
 import pytest
+import torch
 
 import gated_delta_rule_158_b200 as kda
 
@@ -33,3 +34,31 @@ def test_segments_count_towards_the_limit(L):  # noqa: F811
     assert kda.kda_selective_scan_fwd_workspace_size(1, 1 << 20, 8, 8, 1, fits) > 8 * fits
     assert kda.kda_selective_scan_bwd_workspace_size(1, 1 << 20, 8, 8, 1, fits) > 8 * fits
     assert kda.kda_short_conv_bwd_workspace_size(1, 1 << 20, 8, 4, num) > 0
+
+
+def test_binding_refuses_sizes_beyond_32_bits(monkeypatch):
+    """ctypes passes the low 32 bits of an int: 2^32 + 5 tokens would be five."""
+    monkeypatch.setattr(kda._lib.torch.cuda, "current_device", lambda: -1)
+    many = (1 << 32) + 5
+    e = lambda *s, dtype=torch.float32: torch.empty(s, dtype=dtype, device="meta")  # noqa: E731
+    x, w, ws, A = e(1, many, 8), e(8, 4), e(256, dtype=torch.uint8), e(8, 16)
+    bc, q = e(1, many, 1, 16), e(many, 1, 8)
+    cu = e(many, dtype=torch.int32)
+    short = e(1, 5, 8)
+    for call in (lambda: kda.kda_short_conv_fwd(x, w, x, ws),
+                 lambda: kda.kda_short_conv_bwd(x, w, x, dict(dx=x, dweight=w), ws),
+                 lambda: kda.kda_short_conv_step(x[0], w, e(many, 3, 8), x[0]),
+                 lambda: kda.kda_short_conv_fwd(short, w, short, ws, cu_seqlens=cu),
+                 lambda: kda.kda_selective_scan_fwd(x, x, A, bc, bc, x, ws),
+                 lambda: kda.kda_selective_scan_bwd(
+                     x, x, A, bc, bc, x, dict(dx=x, ddelta=x, dA=A, dB=bc, dC=bc), ws),
+                 lambda: kda.kda_selective_scan_step(x[0], x[0], A, bc[0], bc[0], e(many, 8, 16),
+                                                     x[0]),
+                 lambda: kda.kda_qk_norm_fwd(q, q, q, q),
+                 lambda: kda.kda_qk_norm_bwd(q, q, q, q, dict(dq=q, dk=q)),
+                 lambda: kda.kda_short_conv_bwd_workspace_size(1, many, 8, 4),
+                 lambda: kda.kda_selective_scan_fwd_workspace_size(1, many, 8, 16),
+                 lambda: kda.kda_selective_scan_bwd_workspace_size(1, 5, 8, 16, 1, many),
+                 lambda: kda.kda_qk_norm_bwd_workspace_size(many, 1, 1, 8)):
+        with pytest.raises(ValueError, match="2\\^31"):
+            call()
