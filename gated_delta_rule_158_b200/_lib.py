@@ -546,10 +546,13 @@ def kda_selective_scan_fwd_workspace_size(B, T, D, S, G=1, num_seqs=0) -> int:
     return int(lib().kda_selective_scan_fwd_workspace_size(B, T, D, S, G, num_seqs))
 
 
-def _scan_inputs(dev, x, delta, A, Bm, Cm, D, z, delta_bias, delta_softplus):
-    """The marshalled input arguments that the scan's entries share."""
+def _scan_inputs(dev, n, x, delta, A, Bm, Cm, D, z, delta_bias, delta_softplus):
+    """The marshalled input arguments that the scan's entries share; x has `n`
+    dimensions in front of its channels."""
     shape, dt, code = x.shape, x.dtype, _dtype(x)
-    n, ch = len(shape) - 1, shape[-1]
+    if len(shape) != n + 1:
+        raise ValueError(f"x: shape {tuple(shape)}, expected {n + 1} dimensions")
+    ch = shape[-1]
     (S,), (G,) = A.shape[-1:], Bm.shape[-2:-1]
     _sizes(*shape, S, G)
     mix, w = (*shape[:-1], G, S), G * S
@@ -568,8 +571,8 @@ def kda_selective_scan_fwd(x, delta, A, Bm, Cm, out, workspace, D=None, z=None, 
     (inputs may be row slices of wider tensors), A fp32 [D,S], D and delta_bias
     fp32 [D], states fp32 [N,D,S]."""
     dev = torch.cuda.current_device()
+    args, ch, S, G = _scan_inputs(dev, 2, x, delta, A, Bm, Cm, D, z, delta_bias, delta_softplus)
     B, T = x.shape[:2]
-    args, ch, S, G = _scan_inputs(dev, x, delta, A, Bm, Cm, D, z, delta_bias, delta_softplus)
     cu, num, N = _offsets(dev, cu_seqlens, B)
     ws, wsb = _scratch(dev, workspace)
     _check(lib().kda_selective_scan_fwd(
@@ -584,7 +587,7 @@ def kda_selective_scan_step(x, delta, A, Bm, Cm, state, out, D=None, z=None, del
     """One token of N sequences: x, delta, z, out [N,D], Bm, Cm [N,G,S], state
     fp32 [N,D,S] in place."""
     dev = torch.cuda.current_device()
-    args, ch, S, G = _scan_inputs(dev, x, delta, A, Bm, Cm, D, z, delta_bias, delta_softplus)
+    args, ch, S, G = _scan_inputs(dev, 1, x, delta, A, Bm, Cm, D, z, delta_bias, delta_softplus)
     N = x.shape[0]
     _check(lib().kda_selective_scan_step(
         *args, _arg(dev, "state", state, (N, ch, S), _F32T), N, ch, S, G,
@@ -603,8 +606,8 @@ def kda_selective_scan_bwd(x, delta, A, Bm, Cm, dout, grads, workspace, D=None, 
     dict of fp32 outputs dx, ddelta [B,T,D], dA [D,S], dB, dC [B,T,G,S], dz
     [B,T,D] with z, and optionally dD, ddelta_bias [D], d_init [N,D,S]."""
     dev = torch.cuda.current_device()
+    args, ch, S, G = _scan_inputs(dev, 2, x, delta, A, Bm, Cm, D, z, delta_bias, delta_softplus)
     B, T = x.shape[:2]
-    args, ch, S, G = _scan_inputs(dev, x, delta, A, Bm, Cm, D, z, delta_bias, delta_softplus)
     cu, num, N = _offsets(dev, cu_seqlens, B)
     ws, wsb = _scratch(dev, workspace)
     rows, mix, state = (B, T, ch), (B, T, G, S), (N, ch, S)

@@ -62,3 +62,20 @@ def test_binding_refuses_sizes_beyond_32_bits(monkeypatch):
                  lambda: kda.kda_qk_norm_bwd_workspace_size(many, 1, 1, 8)):
         with pytest.raises(ValueError, match="2\\^31"):
             call()
+
+
+def test_binding_refuses_other_numbers_of_dimensions(monkeypatch):
+    """A step of x [N, 2, D] with an output [N, D] would read the first N of its 2 N
+    rows; a prompt of heads [B, T, H, D] the first B T."""
+    monkeypatch.setattr(kda._lib.torch.cuda, "current_device", lambda: -1)
+    e = lambda *s: torch.zeros(s)  # noqa: E731
+    A, ws = e(8, 16), torch.zeros(256, dtype=torch.uint8)
+    x, bc = e(3, 2, 8), e(3, 2, 1, 16)
+    with pytest.raises(ValueError, match="2 dimensions"):
+        kda.kda_selective_scan_step(x, x, A, bc, bc, e(3, 8, 16), e(3, 8))
+    x, bc = e(1, 3, 2, 8), e(1, 3, 2, 1, 16)
+    with pytest.raises(ValueError, match="3 dimensions"):
+        kda.kda_selective_scan_fwd(x, x, A, bc, bc, e(1, 3, 8), ws)
+    grads = dict(dx=e(1, 3, 8), ddelta=e(1, 3, 8), dA=A, dB=e(1, 3, 1, 16), dC=e(1, 3, 1, 16))
+    with pytest.raises(ValueError, match="3 dimensions"):
+        kda.kda_selective_scan_bwd(x, x, A, bc, bc, e(1, 3, 8), grads, ws)
