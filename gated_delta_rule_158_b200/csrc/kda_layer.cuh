@@ -168,8 +168,10 @@ __device__ __forceinline__ float ex2(float x) {
 }
 
 // 1 / (1 + e^-x): e^-x = inf gives 0, NaN stays NaN.  The exponential is off by
-// (2 + |x|) 2^-22 of itself at most and the reciprocal by 2^-23: below 2^-19 of
-// the result for |x| <= 6, and a bf16 rounding is up to 2^-8.
+// (2 + |x|) 2^-22 of itself at most (the unit and its rounded argument), the sum by
+// 2^-24 and the reciprocal by 2^-23: below (3 + |x|) 2^-22 of the result, 2^-18.8
+// for |x| <= 6.  That is far below a bf16 rounding (2^-8); fp32 results carry it,
+// as the header says.
 __device__ __forceinline__ float sigmoid_fast(float x) {
   float y;
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(1.0f + ex2(-kLog2e * x)));

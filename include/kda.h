@@ -391,6 +391,10 @@ KDA_API kda_status kda_recurrent_bwd(const void *q, const void *k, const void *v
  *    a gradient runs in a fixed order, so results are deterministic.
  *  - No output may overlap an input or another output, unless the entry says
  *    so (KDA_ERR_INVALID_ARG).
+ *  - Arithmetic is fp32.  The exponential and the reciprocal of SiLU, gates,
+ *    softplus and decays are the GPU's approximate ones: Sigmoid(x) and e^x are
+ *    within (3 + |x|) 2^-22 of themselves (x = -16: 4.5e-6), for fp32 inputs and
+ *    outputs too, and 0 where they are below 2^-126.
  *  - A workspace belongs to one call at a time: calls, or replays of captured
  *    graphs, that may run side by side need one each.
  *  - B, T >= 1.  cu_seqlens, num_seqs: as kda_chunk_fwd, at most 2^31 - 2^16
@@ -415,7 +419,7 @@ typedef enum kda_activation { KDA_ACT_NONE = 0, KDA_ACT_SILU = 1 } kda_activatio
  *                (init_state rows, then x rows) of each sequence, so that a
  *                later call or kda_short_conv_step continues from it
  *  workspace   : >= 256 bytes (the device status word, cleared by this call)
- * Arithmetic is fp32; out is rounded once.
+ * out is rounded once.
  * Supported: W in {2, 3, 4}, D a multiple of 8, B * T <= 2^31 - 2^16.
  */
 KDA_API kda_status kda_short_conv_fwd(const void *x, int64_t x_stride, const float *weight,
@@ -520,7 +524,17 @@ KDA_API kda_status kda_selective_scan_step(const void *x, int64_t x_stride, cons
  *  dx, ddelta : [B, T, D];  dA : [D, S];  dBm, dCm : [B, T, G, S]
  *  dD_skip, ddelta_bias : [D] or NULL;  dz : [B, T, D], given with z;
  *  d_init : [N, D, S] or NULL
- *  workspace : kda_selective_scan_bwd_workspace_size bytes
+ *  workspace : kda_selective_scan_bwd_workspace_size bytes.  It keeps a state
+ *            for every 8 tokens and the partial sums of dBm and dCm of every
+ *            block of C channels of a group (C = 128, 64, 32, 32, 16 for S = 8,
+ *            16, 32, 64, 128), so it grows with the tokens, by
+ *              D (S + 1) / 2 + 8 S G ceil(D / (G C)) bytes each,
+ *            and by up to 16 D S for every sequence and segment: 42 KiB a token
+ *            at D = 4096, S = 16, G = 1.  A sequence too long for that is passed
+ *            in parts, from the last to the first, with the state in front of
+ *            each part (kda_selective_scan_fwd's final_state) as its init_state
+ *            and the d_init of the part behind it as its d_final; dA, dD_skip
+ *            and ddelta_bias are then sums over a part's own tokens.
  */
 KDA_API size_t kda_selective_scan_bwd_workspace_size(int B, int T, int D, int S, int G,
                                                      int num_seqs);

@@ -353,3 +353,30 @@ def test_norm_gradients_beyond_32_bit_offsets():
         same(g[n][-tail:], a[n], n)
         assert not bool(g[n][-tail - 1000:-tail].any())
         same(g[n + "_weight"], a[n + "_weight"], n + " weight")
+
+
+# ----------------------------------------------------------- gradients in parts
+def test_scan_gradients_in_parts():
+    """A sequence's gradients from its last part to its first, the states passed
+    forward and the state gradients back: those of the whole."""
+    B, T, D, S, cut = 2, 130, 40, 16, 77
+    i = scan_inputs((B, T, D, S, 1, None, True, True, True, True, True, False), F32, seed=61)
+    whole, ws = scan_backward(i, B, T, D, S, 1)
+    ok(ws)
+    part = {}
+    state, d_state = i["init"], i["d_final"]
+    for a, b in ((0, cut), (cut, T)):
+        p = dict(i, init=state)
+        p.update({n: i[n][:, a:b].contiguous() for n in ("x", "delta", "Bm", "Cm", "z", "dout")})
+        part[a] = p
+        _, state, _ = scan_forward(p, B, b - a, D, S, 1)
+    grads = {}
+    for a, b in ((cut, T), (0, cut)):
+        g, ws = scan_backward(dict(part[a], d_final=d_state), B, b - a, D, S, 1)
+        ok(ws)
+        grads[a], d_state = g, g["d_init"]
+    for n in ("dx", "ddelta", "dB", "dC", "dz"):
+        same(torch.cat([grads[0][n], grads[cut][n]], 1), whole[n], n)
+    for n in ("dA", "dD", "ddelta_bias"):
+        same(grads[0][n] + grads[cut][n], whole[n], n)
+    same(grads[0]["d_init"], whole["d_init"], "d_init")
