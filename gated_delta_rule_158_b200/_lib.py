@@ -36,13 +36,6 @@ KDA_NORM_L2 = 1
 KDA_ROT_HALVES = 0
 KDA_ROT_PAIRS = 1
 
-
-def _current_raw_stream(dev):
-    # asked for at the call: a CPU-only torch has no such function, and the
-    # package's host side works there
-    return torch._C._cuda_getCurrentRawStream(dev)
-
-
 _VP = ctypes.c_void_p
 _I = ctypes.c_int
 _I64 = ctypes.c_int64
@@ -167,8 +160,10 @@ def _ptr(t):
 
 def _stream(stream):
     if stream is None:
-        # the handle alone: building a Stream object costs 3 us a call
-        return _current_raw_stream(torch.cuda.current_device())
+        # the handle alone: building a Stream object costs 3 us a call.  The
+        # function is looked up here, since a CPU-only torch has none and the
+        # package's host side works there
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     if isinstance(stream, torch.cuda.Stream):
         return stream.cuda_stream
     return int(stream)
@@ -409,10 +404,12 @@ def _refuse(dev, name, t, shape, dtype):
         raise ValueError(f"{name}: expected a tensor on the current CUDA device")
 
 
-def _sizes(*sizes):
-    """ctypes would cut an int of more than 32 bits down without a word."""
-    if max(sizes) > 0x7FFFFFFF:
-        raise ValueError(f"sizes {sizes}: at most 2^31 - 1 each")
+_INT_MAX = 0x7FFFFFFF  # sizes a, b >= 0: a | b is above it where one of them is
+
+
+def _too_large(*sizes):
+    # ctypes would cut an int of more than 32 bits down without a word
+    raise ValueError(f"sizes {sizes}: at most 2^31 - 1 each")
 
 
 def _rows(dev, name, t, shape, lead, width, dtype):
@@ -462,7 +459,8 @@ def _offsets(dev, cu_seqlens, batch):
     if cu_seqlens is None:
         return None, 0, batch
     n = cu_seqlens.numel() - 1
-    _sizes(n)
+    if n > _INT_MAX:
+        _too_large(n)
     return _arg(dev, "cu_seqlens", cu_seqlens, (n + 1,), torch.int32), n, n
 
 
@@ -474,8 +472,8 @@ def _scratch(dev, workspace):
 
 
 def _on(stream, dev):
-    # the current stream's handle alone: building a Stream object costs 3 us
-    return _current_raw_stream(dev) if stream is None else _stream(stream)
+    # as _stream, for a device that is known
+    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream)
 
 
 def kda_short_conv_fwd(x, weight, out, workspace, bias=None, init_state=None, cu_seqlens=None,
@@ -488,7 +486,8 @@ def kda_short_conv_fwd(x, weight, out, workspace, bias=None, init_state=None, cu
     B, T, D = shape
     W = weight.shape[-1]
     cu, num, N = _offsets(dev, cu_seqlens, B)
-    _sizes(B, T, D, W)
+    if (B | T | D | W) > _INT_MAX:
+        _too_large(B, T, D, W)
     xp, xs = _rows(dev, "x", x, shape, 2, D, dt)
     ws, wsb = _scratch(dev, workspace)
     _check(lib().kda_short_conv_fwd(
@@ -505,7 +504,8 @@ def kda_short_conv_step(x, weight, state, out, bias=None, activation=KDA_ACT_SIL
     shape, dt, code = x.shape, x.dtype, _dtype(x)
     N, D = shape
     W = weight.shape[-1]
-    _sizes(N, D, W)
+    if (N | D | W) > _INT_MAX:
+        _too_large(N, D, W)
     xp, xs = _rows(dev, "x", x, shape, 1, D, dt)
     _check(lib().kda_short_conv_step(
         xp, xs, _arg(dev, "weight", weight, (D, W), _F32T), _opt(dev, "bias", bias, (D,), _F32T),
@@ -514,7 +514,8 @@ def kda_short_conv_step(x, weight, state, out, bias=None, activation=KDA_ACT_SIL
 
 
 def kda_short_conv_bwd_workspace_size(B, T, D, W, num_seqs=0) -> int:
-    _sizes(B, T, D, W, num_seqs)
+    if (B | T | D | W | num_seqs) > _INT_MAX:
+        _too_large(B, T, D, W, num_seqs)
     return int(lib().kda_short_conv_bwd_workspace_size(B, T, D, W, num_seqs))
 
 
@@ -528,7 +529,8 @@ def kda_short_conv_bwd(x, weight, dout, grads, workspace, bias=None, init_state=
     B, T, D = shape
     W = weight.shape[-1]
     cu, num, N = _offsets(dev, cu_seqlens, B)
-    _sizes(B, T, D, W)
+    if (B | T | D | W) > _INT_MAX:
+        _too_large(B, T, D, W)
     xp, xs = _rows(dev, "x", x, shape, 2, D, dt)
     ws, wsb = _scratch(dev, workspace)
     _check(lib().kda_short_conv_bwd(
@@ -542,7 +544,8 @@ def kda_short_conv_bwd(x, weight, dout, grads, workspace, bias=None, init_state=
 
 
 def kda_selective_scan_fwd_workspace_size(B, T, D, S, G=1, num_seqs=0) -> int:
-    _sizes(B, T, D, S, G, num_seqs)
+    if (B | T | D | S | G | num_seqs) > _INT_MAX:
+        _too_large(B, T, D, S, G, num_seqs)
     return int(lib().kda_selective_scan_fwd_workspace_size(B, T, D, S, G, num_seqs))
 
 
@@ -554,7 +557,8 @@ def _scan_inputs(dev, n, x, delta, A, Bm, Cm, D, z, delta_bias, delta_softplus):
         raise ValueError(f"x: shape {tuple(shape)}, expected {n + 1} dimensions")
     ch = shape[-1]
     (S,), (G,) = A.shape[-1:], Bm.shape[-2:-1]
-    _sizes(*shape, S, G)
+    if max(*shape, S, G) > _INT_MAX:
+        _too_large(*shape, S, G)
     mix, w = (*shape[:-1], G, S), G * S
     return (*_rows(dev, "x", x, shape, n, ch, dt), *_rows(dev, "delta", delta, shape, n, ch, dt),
             _arg(dev, "A", A, (ch, S), _F32T), *_rows(dev, "Bm", Bm, mix, n, w, dt),
@@ -595,7 +599,8 @@ def kda_selective_scan_step(x, delta, A, Bm, Cm, state, out, D=None, z=None, del
 
 
 def kda_selective_scan_bwd_workspace_size(B, T, D, S, G=1, num_seqs=0) -> int:
-    _sizes(B, T, D, S, G, num_seqs)
+    if (B | T | D | S | G | num_seqs) > _INT_MAX:
+        _too_large(B, T, D, S, G, num_seqs)
     return int(lib().kda_selective_scan_bwd_workspace_size(B, T, D, S, G, num_seqs))
 
 
@@ -629,8 +634,9 @@ def _norm_inputs(dev, q, k, q_weight, k_weight, positions, inv_freq, mode, rotat
     *lead, Hq, dim = shape
     Hk = k.shape[-2]
     k_shape, n, tokens = (*lead, Hk, dim), len(lead), math.prod(lead)
-    _sizes(tokens, Hq, Hk, dim)
     rot = 0 if inv_freq is None else 2 * inv_freq.numel()
+    if (tokens | Hq | Hk | dim | rot) > _INT_MAX:
+        _too_large(tokens, Hq, Hk, dim, rot)
     return (*_rows(dev, "q", q, shape, n, Hq * dim, dt),
             *_rows(dev, "k", k, k_shape, n, Hk * dim, dt),
             _opt(dev, "q_weight", q_weight, (dim,), _F32T),
@@ -656,7 +662,8 @@ def kda_qk_norm_fwd(q, k, q_out, k_out, q_weight=None, k_weight=None, positions=
 
 
 def kda_qk_norm_bwd_workspace_size(tokens, Hq, Hk, d) -> int:
-    _sizes(tokens, Hq, Hk, d)
+    if (tokens | Hq | Hk | d) > _INT_MAX:
+        _too_large(tokens, Hq, Hk, d)
     return int(lib().kda_qk_norm_bwd_workspace_size(tokens, Hq, Hk, d))
 
 
