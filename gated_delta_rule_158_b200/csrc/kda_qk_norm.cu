@@ -17,7 +17,9 @@
 // 128, bf16, 90 us = 6.0 TB/s (130 us before the blocks stayed and kept rows in
 // flight, 103 us before a group kept to its heads); 8192 tokens x 40 heads with
 // half of each row turned 47 us (the instructions of the turn and the weights,
-// 74 % of the issue slots) and its gradients 79 us = 5.3 TB/s.
+// 74 % of the issue slots; 24 bytes spilled at the 64 registers that four blocks an
+// SM leave) and its gradients 79 us = 5.3 TB/s.  16 tokens x 40 heads: 8 us, one
+// block a token behind its fp64 angles.
 #include <math.h>
 
 #include "kda_layer.cuh"

@@ -21,13 +21,17 @@
 // thread then turns its own into the fp32 rows that the scan reads, token by
 // token.
 //
-// Measured on a B200, bf16, 16 states: 32,768 tokens x 2048 channels in 797 us
-// (18 segments: 357 us for their own end states at 78 % of the special-function
-// unit, 460 us for the outputs at 68 % of it and 59 % of the issue slots; both
-// kernels take as long as their exponentials and their shared-memory words one
-// after the other, and more warps a scheduler gained nothing);
+// Measured on a B200, bf16, 16 states: 32,768 tokens x 2048 channels in 794 us.
+// Under the profiler, each kernel alone and with cold caches, its 18 segments take
+// 355 us for their own end states (79 % of the special-function unit), 9 us for the
+// combination and 461 us for the outputs (68 % of that unit, 58 % of the issue
+// slots).  Both large kernels take as long as their exponentials and their
+// shared-memory words one after the other, and more warps a scheduler gained
+// nothing.  Of those words half or more are B and C, which for bf16 inputs are
+// widened before shared memory; each tile of 32 tokens forms the decays of 34.
 // 12,001 packed tokens x 4096 in 400 to 450 us.  One token of 256 sequences x 4096: 32
-// us = 4.4 TB/s.  Tried and not kept: one state a thread (878 us for the long
+// us = 4.4 TB/s (a thread loads its states once, computes and stores: nothing is in
+// flight meanwhile, at 68 % of the issue slots).  Tried and not kept: one state a thread (878 us for the long
 // prompt's outputs: its loads), a quarter of the exponentials as polynomials on
 // the multiply-add units (472 us instead of 460), tiles of 16 tokens (481 us), five
 // or six CTAs an SM (462 us).

@@ -25,8 +25,8 @@
 // where each exchanged value costs a shuffle, two selects and an addition.
 //
 // Measured on a B200, bf16, 16 states, 4 x 4096 tokens x 2048 channels: 287 us
-// for the segments' pass, 673 us for the walk (55 % of the issue slots at two
-// warps a scheduler), 21 us for the sums.  One channel a thread and 16 tokens a
+// for the segments' pass, 669 us for the walk (55 % of the issue slots at two
+// warps a scheduler; 255 registers, 8 bytes of them spilled), 20 us for the sums.  One channel a thread and 16 tokens a
 // tile took 1715 us; the walk in one wave of CTAs instead of four, 750 us; three
 // warps a scheduler at 168 registers spill (800 us); dt, u and dy stored twice,
 // so that the pairs need no moves, load half as much again (771 us).
