@@ -380,3 +380,34 @@ def test_scan_gradients_in_parts():
     for n in ("dA", "dD", "ddelta_bias"):
         same(grads[0][n] + grads[cut][n], whole[n], n)
     same(grads[0]["d_init"], whole["d_init"], "d_init")
+
+
+# ------------------------------------------------------------- sigmoid, element by element
+def test_silu_and_gate_elementwise():
+    """fp32 callers' SiLU and gate: the sigmoid within (3 + |x|) 2^-22 of itself, and
+    a rounding (2^-24) for each product behind it.  A tap of one and zeros make the
+    convolution x sigmoid(x); B = C = 0 and a skip of one make the scan z sigmoid(z)."""
+    v = torch.cat([torch.linspace(-80, 80, 4089), torch.tensor([0.0, -0.0, 1e-30, -1e-30, 1e-4,
+                                                                -1e-4, 20.0])]).to(DEV)
+    D = v.numel()
+    assert D % 8 == 0
+    w = torch.zeros(D, 2, device=DEV)
+    w[:, 1] = 1
+    outs = [torch.empty(1, 1, D, device=DEV) for _ in range(4)]
+    ws = torch.empty(kda.kda_selective_scan_fwd_workspace_size(1, 1, D, 8), dtype=torch.uint8,
+                     device=DEV)
+    kda.kda_short_conv_fwd(v.view(1, 1, D), w, outs[0], ws)
+    kda.kda_short_conv_step(v.view(1, D), w, torch.zeros(1, 1, D, device=DEV), outs[1][0])
+    one, none, A = torch.ones(1, 1, D, device=DEV), torch.zeros(1, 1, 1, 8, device=DEV), \
+        torch.zeros(D, 8, device=DEV)
+    opt = dict(D=one.view(D), z=v.view(1, 1, D))
+    kda.kda_selective_scan_fwd(one, one, A, none, none, outs[2], ws, **opt)
+    opt["z"] = v.view(1, D)
+    kda.kda_selective_scan_step(one[0], one[0], A, none[0], none[0],
+                                torch.zeros(1, D, 8, device=DEV), outs[3][0], **opt)
+    x = v.cpu().double()
+    ref = x * torch.sigmoid(x)
+    bar = ref.abs() * ((3 + x.abs()) * 2.0 ** -22 + 2 * 2.0 ** -24)
+    for out in outs:
+        err = (out.view(D).cpu().double() - ref).abs()
+        assert bool((err <= bar).all()), float((err / ref.abs()).nan_to_num().max())
