@@ -3,7 +3,6 @@
 #pragma once
 
 #include <float.h>
-#include <math.h>
 
 #include "kda_layer.cuh"
 
@@ -137,8 +136,9 @@ constexpr float kNudge = 2.9e-8f;
 // finite value: the tokens behind a segment's end have dt = 0, and 0 * inf would
 // be NaN; any dt above 2^-120 still gives 0.
 __device__ __forceinline__ float rate2(float A) {
-  const float r = A * kLog2e;
-  return r == -INFINITY ? -FLT_MAX : r;
+  float r;  // NaN stays NaN
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(A * kLog2e), "f"(-FLT_MAX));
+  return r;
 }
 __device__ __forceinline__ float decay(float dt, float A2) { return ex2(fmaf(dt, A2, kNudge)); }
 __device__ __forceinline__ f2 decay_exp(f2 dt, f2 A2) {

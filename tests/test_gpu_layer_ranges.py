@@ -411,3 +411,13 @@ def test_silu_and_gate_elementwise():
     for out in outs:
         err = (out.view(D).cpu().double() - ref).abs()
         assert bool((err <= bar).all()), float((err / ref.abs()).nan_to_num().max())
+
+
+def test_scan_nan_in_a_rate_stays_in_its_channel():
+    i = scan_inputs((2, 33, 40, 16, 1, None, True, True, True, True, True, False), F32, seed=41)
+    clean = scan_forward(i, 2, 33, 40, 16, 1)[:2]
+    i["A"][7, 3] = float("nan")
+    out, fin, _ = scan_forward(i, 2, 33, 40, 16, 1)
+    assert bool(torch.isnan(out[..., 7]).all()) and bool(torch.isnan(fin[:, 7, 3]).all())
+    out[..., 7], fin[:, 7, 3] = clean[0][..., 7], clean[1][:, 7, 3]
+    assert torch.equal(out, clean[0]) and torch.equal(fin, clean[1])
