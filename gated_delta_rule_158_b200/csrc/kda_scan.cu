@@ -29,7 +29,7 @@
 // shared-memory words one after the other, and more warps a scheduler gained
 // nothing.  Of those words half or more are B and C, which for bf16 inputs are
 // widened before shared memory; each tile of 32 tokens forms the decays of 34.
-// 12,001 packed tokens x 4096 in 400 to 450 us.  One token of 256 sequences x 4096: 32
+// 12,001 packed tokens x 4096 in 390 to 450 us.  One token of 256 sequences x 4096: 32
 // us = 4.4 TB/s (a thread loads its states once, computes and stores: nothing is in
 // flight meanwhile, at 68 % of the issue slots).  Tried and not kept: one state a thread (878 us for the long
 // prompt's outputs: its loads), a quarter of the exponentials as polynomials on
